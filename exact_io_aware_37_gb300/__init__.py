@@ -11,7 +11,9 @@ Layouts: dense tensors are [B, H, N, D]; packed variable-length batches are
 [H, T, D] with int32 ``cu_seqlens`` [B + 1] on the device and ``max_seqlen``.
 """
 
+import contextlib
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -20,7 +22,10 @@ from ._lib import FA_BF16, FA_F16, FA_F32, FAError, lib, library_path  # noqa: F
 __all__ = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_get_last_device_error", "fa_strerror",
            "fa_set_wait_limit_ns", "fa_selftest_wait_timeout", "fa_selftest_tile", "fa_path_name", "fa_launch_count", "fa_bwd_static_ws", "fa_bwd_time_main_kernel", "forward", "backward",
            "fa_decode", "fa_decode_workspace_size", "decode", "fa_fwd_dropout", "fa_bwd_dropout",
-           "fa_bwd_deterministic", "fa_probe_ex2_rate", "FAError"]
+           "fa_bwd_deterministic", "fa_probe_ex2_rate", "FAError",
+           "Cache8", "cache_alloc", "fa_cache_write", "fa_cache_read", "cache_read", "fa_decode_cache",
+           "fa_decode_cache_workspace_size", "decode_cache", "fa_decode_shared", "fa_decode_shared_workspace_size",
+           "decode_shared"]
 
 _DT = {torch.bfloat16: FA_BF16, torch.float32: FA_F32, torch.float16: FA_F16}
 
@@ -283,3 +288,218 @@ def backward(q, k, v, o, lse, dout, causal=False, scale=None, cu_seqlens=None, m
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd(q, k, v, o, lse, dout, dq, dk, dv, causal, scale, cu_seqlens, max_seqlen, workspace, stream)
     return dq, dk, dv
+
+
+# ---- cached serving: the 8-bit cache and the decoding steps that read it ----
+
+class Cache8(NamedTuple):
+    """An 8-bit key/value cache: k, v [B, Hk, cap, D] e4m3 codes
+    (torch.float8_e4m3fn) and k_exp, v_exp [B, Hk, cap] uint8, one exponent
+    byte a row; value = code * 2^(exp - 127)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+
+
+def cache_alloc(B, Hk, cap, D, device="cuda"):
+    """An empty 8-bit cache (codes and exponents zero) for B sequences of at
+    most cap rows and Hk key heads."""
+    k, v = (torch.zeros(B, Hk, cap, D, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+    k_exp, v_exp = (torch.zeros(B, Hk, cap, dtype=torch.uint8, device=device) for _ in range(2))
+    return Cache8(k, v, k_exp, v_exp)
+
+
+def _check_cuda(*tensors):
+    """_check, and that the tensors (the first one sets the device) are on a GPU."""
+    if not tensors[0].is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    _check(*tensors)
+
+
+@contextlib.contextmanager
+def _other(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t, stream):
+    """Makes t's device and `stream` (None: that device's current one) current
+    for a call, so that its scratch and outputs are allocated for the stream
+    that writes them."""
+    if stream is None and t.get_device() == torch.cuda.current_device():
+        return _HERE
+    return _other(t.device, stream)
+
+
+def _check_cache8(cache):
+    k, v, k_exp, v_exp = cache
+    if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k.shape[:3]:
+        raise ValueError("a cache holds k, v [B, Hk, cap, D] and k_exp, v_exp [B, Hk, cap]")
+    if k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype:
+        raise ValueError("cache codes must be float8_e4m3fn")
+    if k_exp.dtype != torch.uint8 or v_exp.dtype != torch.uint8:
+        raise ValueError("cache exponents must be uint8")
+
+
+def _check_int32(name, t, B):
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B):
+        raise ValueError(f"{name} must be int32 [{B}]")
+
+
+def _raise(st, where):
+    if st != 0:
+        raise FAError(st, where)
+
+
+def _rows_call(fn, where, k, v, cache, start, count, stream):
+    cache = Cache8(*cache)
+    _check_cuda(k, v, *cache, start, count)
+    _check_cache8(cache)
+    B, H, cap, D = cache.k.shape
+    if k.dim() != 4 or v.shape != k.shape or (k.shape[0], k.shape[1], k.shape[3]) != (B, H, D):
+        raise ValueError("k and v must be [B, Hk, n, D] with the cache's B, Hk and D")
+    if v.dtype != k.dtype or k.dtype not in _DT:
+        raise ValueError("k and v must be both bfloat16, float16 or float32")
+    _check_int32("start", start, B)
+    _check_int32("count", count, B)
+    n = k.shape[2]
+    dense, held = (_ptr(k), _ptr(v)), tuple(map(_ptr, cache))
+    with _on(k, stream):
+        _raise(fn(*(dense + held if where == "fa_cache_write" else held + dense), B, H, n, cap, D, _ptr(start),
+                  _ptr(count), _DT[k.dtype], _stream(stream)), where)
+
+
+def fa_cache_write(k, v, cache, start=None, count=None, stream=None):
+    """Quantise new rows k, v [B, Hk, n, D] (bf16, fp16 or fp32) into the 8-bit
+    cache at rows start[b] .. start[b] + count[b] - 1 of every sequence (start,
+    count: int32 [B] on the device; None: 0 and n).  Rows that are not
+    addressed keep what they hold; a sequence whose range does not fit in the
+    cache is skipped and reported by fa_get_last_device_error."""
+    _rows_call(lib().fa_cache_write, "fa_cache_write", k, v, cache, start, count, stream)
+
+
+def fa_cache_read(cache, k, v, start=None, count=None, stream=None):
+    """Read rows start[b] .. start[b] + count[b] - 1 of the 8-bit cache into k,
+    v [B, Hk, n, D] (bf16, fp16 or fp32); the rows after them become zeros."""
+    _rows_call(lib().fa_cache_read, "fa_cache_read", k, v, cache, start, count, stream)
+
+
+def cache_read(cache, start, n, count=None, dtype=torch.bfloat16, stream=None):
+    """Allocating wrapper around fa_cache_read: returns (k, v) [B, Hk, n, D]."""
+    B, H, _, D = cache[0].shape
+    with _on(cache[0], stream):
+        k, v = (torch.empty(B, H, n, D, dtype=dtype, device=cache[0].device) for _ in range(2))
+    fa_cache_read(cache, k, v, start, count, stream)
+    return k, v
+
+
+def _serve_dims(q, cache, max_len):
+    """(B, H, Hk, nq, cap, max_len, D) of a decoding step over a cache."""
+    if q.dim() != 4 or cache[0].dim() != 4:
+        raise ValueError("q must be [B, H, nq, D] and the cache [B, Hk, cap, D]")
+    B, H, nq, D = q.shape
+    Bk, Hk, cap, Dk = cache[0].shape
+    if Bk != B or Dk != D or Hk == 0 or H % Hk:
+        raise ValueError("q [B, H, nq, D] needs a cache [B, Hk, cap, D] with H a multiple of Hk")
+    max_len = cap if max_len is None else int(max_len)
+    if not 0 <= max_len <= cap:
+        raise ValueError("max_len must be between 0 and the cache's capacity")
+    return B, H, Hk, nq, cap, max_len, D
+
+
+def _serve_call(where, q, prefix, cache, lens, o, lse, causal, scale, max_len, workspace, stream):
+    B, H, Hk, nq, cap, max_len, D = _serve_dims(q, cache, max_len)
+    if len(cache) == 4:
+        _check_cache8(cache)
+    elif len(cache) != 2 or cache[1].shape != cache[0].shape or cache[0].dtype != q.dtype or cache[1].dtype != q.dtype:
+        raise ValueError("the cache must be a Cache8, or a pair k, v [B, Hk, cap, D] of q's dtype")
+    _check_cuda(q, *prefix, *cache, lens, o, lse, workspace)
+    if q.dtype not in _DT or o.dtype != q.dtype or o.shape != q.shape:
+        raise ValueError("o must have q's shape and dtype")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
+        raise ValueError("lse must be float32 [B, H, nq]")
+    _check_int32("lens", lens, B)
+    np_ = 0
+    if prefix:
+        kp, vp = prefix
+        if kp.dim() != 3 or vp.shape != kp.shape or kp.shape[0] != Hk or kp.shape[2] != D:
+            raise ValueError("the prefix must be k, v [Hk, np, D]")
+        if kp.dtype != q.dtype or vp.dtype != q.dtype:
+            raise ValueError("the prefix must have q's dtype")
+        np_ = kp.shape[1]
+    dt = _DT[q.dtype]
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    with _on(q, stream):
+        if workspace is None:
+            need = lib().fa_decode_shared_workspace_size(B, H, Hk, nq, np_, max_len, D, dt)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        head = (_ptr(q),) + (tuple(map(_ptr, prefix)) if prefix else ())
+        held = tuple(map(_ptr, cache)) if len(cache) == 4 else (_ptr(cache[0]), _ptr(cache[1]), None, None)
+        sizes = (B, H, Hk, nq, np_, cap, max_len, D) if prefix else (B, H, Hk, nq, cap, max_len, D)
+        _raise(getattr(lib(), where)(*head, *held, _ptr(o), _ptr(lse), *sizes, scale, int(bool(causal)), _ptr(lens), dt,
+                                     _ptr(workspace), nbytes, _stream(stream)), where)
+
+
+def fa_decode_cache_workspace_size(q, cache, max_len=None):
+    """Bytes of scratch fa_decode_cache needs for q [B, H, nq, D] and this cache."""
+    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache, max_len)
+    return int(lib().fa_decode_cache_workspace_size(B, H, Hk, nq, max_len, D, _DT[q.dtype]))
+
+
+def fa_decode_cache(q, cache, lens, o, lse, causal, scale=None, max_len=None, workspace=None, stream=None):
+    """Enqueue a decoding step over an 8-bit cache: the new queries q [B, H, nq,
+    D] (bf16 or fp16) against the first lens[b] rows (int32 [B] on the device;
+    None: max_len) of each sequence, the new tokens' rows among them.  H must be
+    a multiple of the cache's Hk; query head h reads key head h // (H // Hk).
+    Query i is at position lens[b] - nq + i.  max_len (default: the capacity)
+    bounds lens.  Writes o (dtype of q) and lse [B, H, nq] (float32); rows that
+    see no key get 0 and -inf."""
+    cache = Cache8(*cache)
+    _serve_call("fa_decode_cache", q, (), cache, lens, o, lse, causal, scale, max_len, workspace, stream)
+
+
+def decode_cache(q, cache, lens=None, causal=True, scale=None, max_len=None, stream=None):
+    """Allocating wrapper around fa_decode_cache: returns (o, lse)."""
+    with _on(q, stream):
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fa_decode_cache(q, cache, lens, o, lse, causal, scale, max_len, stream=stream)
+    return o, lse
+
+
+def fa_decode_shared_workspace_size(q, k_prefix, cache, max_len=None):
+    """Bytes of scratch fa_decode_shared needs for q [B, H, nq, D], a prefix
+    k_prefix [Hk, np, D] and the sequences' own cache."""
+    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache, max_len)
+    return int(lib().fa_decode_shared_workspace_size(B, H, Hk, nq, k_prefix.shape[1], max_len, D, _DT[q.dtype]))
+
+
+def fa_decode_shared(q, k_prefix, v_prefix, cache, lens, o, lse, causal, scale=None, max_len=None, workspace=None,
+                     stream=None):
+    """Enqueue a decoding step of a batch whose sequences share their first np
+    keys: k_prefix, v_prefix [Hk, np, D] (dtype of q), then lens[b] rows of
+    each sequence's own, in `cache`: a Cache8, or a pair k, v [B, Hk, cap, D] of
+    q's dtype.  Query i is at position np + lens[b] - nq + i.  Everything else
+    as for fa_decode_cache."""
+    _serve_call("fa_decode_shared", q, (k_prefix, v_prefix), tuple(cache), lens, o, lse, causal, scale, max_len,
+                workspace, stream)
+
+
+def decode_shared(q, k_prefix, v_prefix, cache, lens=None, causal=True, scale=None, max_len=None, stream=None):
+    """Allocating wrapper around fa_decode_shared: returns (o, lse)."""
+    with _on(q, stream):
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fa_decode_shared(q, k_prefix, v_prefix, cache, lens, o, lse, causal, scale, max_len, stream=stream)
+    return o, lse

@@ -41,6 +41,12 @@ SIGNATURES = {
                                     _vp, _int, _int, _f, _c.c_uint64, _c.c_uint32, _vp, _sz, _vp]),
     "fa_decode_workspace_size": (_sz, [_int, _int, _int, _int, _int, _int]),
     "fa_probe_ex2_rate": (_int, [_int, _c.POINTER(_c.c_double), _vp]),
+    "fa_cache_write": (_int, [_vp] * 6 + [_int] * 5 + [_vp, _vp, _int, _vp]),
+    "fa_cache_read": (_int, [_vp] * 6 + [_int] * 5 + [_vp, _vp, _int, _vp]),
+    "fa_decode_cache_workspace_size": (_sz, [_int] * 7),
+    "fa_decode_cache": (_int, [_vp] * 7 + [_int] * 7 + [_f, _int, _vp, _int, _vp, _sz, _vp]),
+    "fa_decode_shared_workspace_size": (_sz, [_int] * 8),
+    "fa_decode_shared": (_int, [_vp] * 9 + [_int] * 8 + [_f, _int, _vp, _int, _vp, _sz, _vp]),
     "fa_decode": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _f, _int, _int, _vp, _sz, _vp]),
 }
 

@@ -443,4 +443,123 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+static fa_status cache_rows(const void* k, const void* v, const void* k_codes, const void* v_codes,
+                            const uint8_t* k_exp, const uint8_t* v_exp, int B, int H, int n, int cap, int D,
+                            const int32_t* start, const int32_t* count, fa_dtype dtype, bool write, void* stream) {
+  if (B < 0 || H < 0 || n < 0 || cap < 0 || D <= 0) return FA_ERR_INVALID;
+  if (n > cap) return FA_ERR_INVALID;
+  if (dtype != FA_BF16 && dtype != FA_F32 && dtype != FA_F16) return FA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 65535 || (long long)B * H > (1ll << 30) ||
+      (long long)B * H * (n > 0 ? n : 1) > (1ll << 31) - 1)
+    return FA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+  if (B == 0 || H == 0 || n == 0) return FA_OK;
+  fa_status st;
+  for (const void* p : {k, v, k_codes, v_codes})
+    if ((st = check_tensor(p)) != FA_OK) return st;
+  if (k_exp == nullptr || v_exp == nullptr) return FA_ERR_INVALID;
+  for (const int32_t* p : {start, count})
+    if (p != nullptr && !aligned(p, 4)) return FA_ERR_ALIGN;
+  CacheRows a{};
+  a.k = k; a.v = v;
+  a.k_codes = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+  a.v_codes = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+  a.k_exp = const_cast<uint8_t*>(k_exp);
+  a.v_exp = const_cast<uint8_t*>(v_exp);
+  a.H = H; a.n = n; a.cap = cap;
+  a.rows = (uint32_t)((long long)B * H * n);
+  a.start = start; a.count = count;
+  g_detail[0] = 0;
+  if (note_error("status word", status_word(&a.status)) != cudaSuccess) return FA_ERR_CUDA;
+  return launch_cache8(a, D, dtype, write, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_write(const void* k, const void* v, void* k_codes, void* v_codes, uint8_t* k_exp, uint8_t* v_exp,
+                         int B, int H, int n, int cap, int D, const int32_t* start, const int32_t* count,
+                         fa_dtype dtype, void* stream) {
+  return cache_rows(k, v, k_codes, v_codes, k_exp, v_exp, B, H, n, cap, D, start, count, dtype, true, stream);
+}
+
+fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t* k_exp, const uint8_t* v_exp, void* k,
+                        void* v, int B, int H, int n, int cap, int D, const int32_t* start, const int32_t* count,
+                        fa_dtype dtype, void* stream) {
+  return cache_rows(k, v, k_codes, v_codes, k_exp, v_exp, B, H, n, cap, D, start, count, dtype, false, stream);
+}
+
+// Sizes of a decoding step over a cache (the prefix: np keys, 0 without one).
+static fa_status serve_sizes(int B, int H, int Hk, int nq, int np, int cap, int max_len, int D, fa_dtype dt) {
+  if (B < 0 || H < 0 || Hk < 0 || nq < 0 || np < 0 || cap < 0 || max_len < 0 || D <= 0) return FA_ERR_INVALID;
+  if (max_len > cap) return FA_ERR_INVALID;
+  if (H > 0 && (Hk == 0 || H % Hk != 0)) return FA_ERR_INVALID;
+  if (dt != FA_BF16 && dt != FA_F16) return FA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * H > (1ll << 30) || (long long)B * H * (nq > 0 ? nq : 1) > (1ll << 31) - 1 ||
+      (long long)np + max_len > (1ll << 31) - 1)
+    return FA_ERR_UNSUPPORTED;  // rows and keys are counted in 32 bits
+  return FA_OK;
+}
+
+static fa_status serve(const void* q, const void* kp, const void* vp, const void* k, const void* v,
+                       const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk, int nq,
+                       int np, int cap, int max_len, int D, float scale, int causal, const int32_t* lens, fa_dtype dt,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = serve_sizes(B, H, Hk, nq, np, cap, max_len, D, dt);
+  if (st != FA_OK) return st;
+  if (!scale_ok(scale)) return FA_ERR_INVALID;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID;
+  if (B == 0 || H == 0 || nq == 0) return FA_OK;
+  for (const void* p : {q, (const void*)o})
+    if ((st = check_tensor(p)) != FA_OK) return st;
+  if (np > 0)
+    for (const void* p : {kp, vp})
+      if ((st = check_tensor(p)) != FA_OK) return st;
+  if (max_len > 0)  // an empty cache has no rows to point at
+    for (const void* p : {k, v})
+      if ((st = check_tensor(p)) != FA_OK) return st;
+  if (lse == nullptr) return FA_ERR_INVALID;
+  if (!aligned(lse, 4) || (lens != nullptr && !aligned(lens, 4))) return FA_ERR_ALIGN;
+  const size_t need = serve_workspace_bytes(B, H, Hk, nq, np, max_len, D);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+
+  ServeArgs a{};
+  a.q = q; a.kp = kp; a.vp = vp; a.k = k; a.v = v;
+  a.k_exp = k_exp; a.v_exp = v_exp;
+  a.o = o; a.lse = lse;
+  a.B = B; a.Hk = Hk; a.group = H / Hk; a.nq = nq; a.np = np; a.cap = cap; a.max_len = max_len;
+  a.lens = lens;
+  a.c2 = scale * kLog2e;
+  a.causal = causal;
+  g_detail[0] = 0;
+  if (note_error("status word", status_word(&a.status)) != cudaSuccess) return FA_ERR_CUDA;
+  return launch_serve(a, D, dt, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_decode_cache_workspace_size(int B, int H, int Hk, int nq, int max_len, int D, fa_dtype dt) {
+  return fa_decode_shared_workspace_size(B, H, Hk, nq, 0, max_len, D, dt);
+}
+
+fa_status fa_decode_cache(const void* q, const void* k_codes, const void* v_codes, const uint8_t* k_exp,
+                          const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk, int nq, int cap, int max_len,
+                          int D, float scale, int causal, const int32_t* lens, fa_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (max_len > 0 && (k_exp == nullptr || v_exp == nullptr)) return FA_ERR_INVALID;
+  return serve(q, nullptr, nullptr, k_codes, v_codes, k_exp, v_exp, o, lse, B, H, Hk, nq, 0, cap, max_len, D, scale,
+               causal, lens, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t fa_decode_shared_workspace_size(int B, int H, int Hk, int nq, int np, int max_len, int D, fa_dtype dt) {
+  if (B <= 0 || H <= 0 || nq <= 0 || serve_sizes(B, H, Hk, nq, np, max_len, max_len, D, dt) != FA_OK) return 0;
+  return serve_workspace_bytes(B, H, Hk, nq, np, max_len, D);
+}
+
+fa_status fa_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                           const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk,
+                           int nq, int np, int cap, int max_len, int D, float scale, int causal, const int32_t* lens,
+                           fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if ((k_exp == nullptr) != (v_exp == nullptr)) return FA_ERR_INVALID;
+  return serve(q, k_prefix, v_prefix, k, v, k_exp, v_exp, o, lse, B, H, Hk, nq, np, cap, max_len, D, scale, causal,
+               lens, dtype, workspace, workspace_bytes, stream);
+}
+
 }  // extern "C"

@@ -175,4 +175,45 @@ DecodeSplit decode_split(int B, int H, int nq, int nk);
 size_t decode_workspace_bytes(int B, int H, int nq, int nk, int D);
 cudaError_t launch_decode(const Problem& p, int nq, int nk, fa_dtype dt, void* workspace, cudaStream_t s);
 
+// Rows to write into or read from the 8-bit cache (fa_cache8.cu): n dense rows
+// of every (b, h), of which the first count[b] are at start[b] in the cache.
+struct CacheRows {
+  const void* k;  // dense [B, H, n, D]: the source of a write, the destination of a read
+  const void* v;
+  uint8_t* k_codes;  // [B, H, cap, D]
+  uint8_t* v_codes;
+  uint8_t* k_exp;  // [B, H, cap]
+  uint8_t* v_exp;
+  int H, n, cap;
+  uint32_t rows;  // B * H * n
+  const int32_t* start;  // device, or nullptr: 0
+  const int32_t* count;  // device, or nullptr: n
+  unsigned* status;
+};
+cudaError_t launch_cache8(const CacheRows& a, int D, fa_dtype dt, bool write, cudaStream_t s);
+
+// Decoding over a cache with lengths of its own for every sequence, grouped
+// heads and an optional shared prefix (fa_decode_cache.cu).
+struct ServeArgs {
+  const void* q;   // [B, Hk * group, nq, D]
+  const void* kp;  // the prefix [Hk, np, D] (np > 0)
+  const void* vp;
+  const void* k;  // [B, Hk, cap, D]: codes when k_exp is given, else 16-bit values
+  const void* v;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  void* o;
+  float* lse;
+  int B, Hk, group, nq, np, cap, max_len;
+  const int32_t* lens;  // device, or nullptr: max_len each
+  float c2;             // scale * log2(e)
+  int causal;
+  unsigned* status;
+  float* part_u;
+  float* part_ml;
+  int splits, keys_per_split;
+};
+size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, int D);
+cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s);
+
 }  // namespace fa

@@ -377,6 +377,77 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
                     int D, float scale, int causal, fa_dtype dtype, void* workspace, size_t workspace_bytes,
                     void* stream);
 
+/* ---- cached serving: an 8-bit cache, grouped heads, unequal lengths, a shared prefix ----
+ *
+ * These entry points extend the cached decoding step (tensortonic.com
+ * "FlashAttention" section 8) to what a server holds: sequences of unlike length
+ * in one cache of fixed capacity, kept in 8 bits, behind a prompt they share.
+ * The pages have no counterpart beyond the step itself.
+ *
+ * The 8-bit cache: for every (sequence b, key head h, position p < cap) the D
+ * values of a key (value) row are held as D e4m3 codes [B, Hk, cap, D] and one
+ * exponent byte x [B, Hk, cap], meaning code * 2^(x - 127).  The exponent is
+ * the smallest in -127 .. 120 for which the row's largest finite magnitude is
+ * at most 448; a row without a nonzero finite value has x = 0.  Codes are
+ * rounded to nearest even; infinities and NaN become the NaN code.  D must be
+ * 64 or 128.
+ *
+ * Device-side ranges and lengths (start, count, lens: DEVICE int32[B]) are
+ * checked by the kernels: a sequence whose values are out of range is skipped,
+ * its outputs are left as they were, and FA_ERR_INVALID is latched
+ * (fa_get_last_device_error).  All calls are asynchronous, allocate nothing and
+ * can be captured in a CUDA graph under the conditions above; a replay reads
+ * the lengths that the buffers hold then. */
+
+/* Quantises new rows into the cache.
+ *   k, v     in : [B, H, n, D], dtype (all three)
+ *   k_codes, v_codes, k_exp, v_exp   the cache, written at positions start[b] + i for i < count[b] only
+ *   start    NULL: 0 for every sequence
+ *   count    NULL: n; else 0 <= count[b] <= n, and start[b] + count[b] <= cap
+ * n <= cap; B * H * n < 2^31 (FA_ERR_UNSUPPORTED). */
+fa_status fa_cache_write(const void* k, const void* v, void* k_codes, void* v_codes, uint8_t* k_exp, uint8_t* v_exp,
+                         int B, int H, int n, int cap, int D, const int32_t* start, const int32_t* count,
+                         fa_dtype dtype, void* stream);
+
+/* Reads rows of the cache back: k, v [B, H, n, D] in dtype, each value rounded
+ * to nearest once (exact in float32 up to its largest value; in bf16 unless it is subnormal there).
+ * Rows i >= count[b] are written as zeros.  Arguments as for fa_cache_write. */
+fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t* k_exp, const uint8_t* v_exp, void* k,
+                        void* v, int B, int H, int n, int cap, int D, const int32_t* start, const int32_t* count,
+                        fa_dtype dtype, void* stream);
+
+/* Decoding step over the 8-bit cache.
+ *   q     [B, H, nq, D] the new queries, bf16 or fp16 (FA_ERR_UNSUPPORTED for float32)
+ *   codes, exponents: the cache [B, Hk, cap, D] and [B, Hk, cap], the new tokens' rows included; query head h
+ *         reads key head h / (H / Hk); H must be a multiple of Hk (FA_ERR_INVALID)
+ *   lens  keys of each sequence, 0 <= lens[b] <= max_len <= cap; NULL: max_len each.  Rows at and after lens[b]
+ *         are never used, whatever they hold
+ *   o     [B, H, nq, D] written (dtype);  lse [B, H, nq] float32, natural log
+ * Query row i sits at position lens[b] - nq + i, so causal allows key j iff j <= i + lens[b] - nq.  Rows with no
+ * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32; the weights are rounded to
+ * fp16 for their product with the values.
+ * workspace: DEVICE scratch of fa_decode_cache_workspace_size(...) bytes, 256-byte aligned, owned by the caller; its
+ * contents do not matter; calls (and graph replays) that overlap on the GPU need workspaces of their own. */
+size_t fa_decode_cache_workspace_size(int B, int H, int Hk, int nq, int max_len, int D, fa_dtype dtype);
+fa_status fa_decode_cache(const void* q, const void* k_codes, const void* v_codes, const uint8_t* k_exp,
+                          const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk, int nq, int cap, int max_len,
+                          int D, float scale, int causal, const int32_t* lens, fa_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Decoding step of a batch whose sequences share their first np keys, which are read once for all.
+ *   k_prefix, v_prefix  [Hk, np, D], dtype (may be NULL when np == 0)
+ *   k, v                the sequences' own rows, at most max_len of each: [B, Hk, cap, D] in dtype when k_exp and
+ *                       v_exp are NULL, else the 8-bit cache's codes with its exponents (may be NULL when
+ *                       max_len == 0)
+ * The keys of sequence b are the prefix, then its own lens[b] rows: query row i sits at position
+ * np + lens[b] - nq + i of them.  Everything else is as for fa_decode_cache; with 16-bit rows of its own the weights
+ * are rounded to dtype.  np + max_len < 2^31. */
+size_t fa_decode_shared_workspace_size(int B, int H, int Hk, int nq, int np, int max_len, int D, fa_dtype dtype);
+fa_status fa_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                           const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk,
+                           int nq, int np, int cap, int max_len, int D, float scale, int causal, const int32_t* lens,
+                           fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
