@@ -495,7 +495,7 @@ static fa_status serve_sizes(int B, int H, int Hk, int nq, int np, int cap, int 
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (B > 65535 || H > 65535) return FA_ERR_UNSUPPORTED;
   if ((long long)B * H > (1ll << 30) || (long long)B * H * (nq > 0 ? nq : 1) > (1ll << 31) - 1 ||
-      (long long)np + max_len > (1ll << 31) - 1)
+      (long long)np + max_len > (1ll << 30))
     return FA_ERR_UNSUPPORTED;  // rows and keys are counted in 32 bits
   return FA_OK;
 }
@@ -528,6 +528,7 @@ static fa_status serve(const void* q, const void* kp, const void* vp, const void
   a.o = o; a.lse = lse;
   a.B = B; a.Hk = Hk; a.group = H / Hk; a.nq = nq; a.np = np; a.cap = cap; a.max_len = max_len;
   a.lens = lens;
+  a.wait_limit_ns = g_wait_limit_ns.load();
   a.c2 = scale * kLog2e;
   a.causal = causal;
   g_detail[0] = 0;

@@ -12,6 +12,8 @@
 
 #include "fa_cache8.cuh"
 #include "fa_internal.cuh"
+#include "fa_serve.cuh"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
@@ -19,10 +21,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kG = 8;  // query rows per CTA
-
-// Factor of a state with maximum m joined under the maximum mm >= m: 1 for
-// equal maxima, -inf among them (that state holds nothing, or only NaN).
-__device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }
 
 template <typename T, int E>
 __device__ __forceinline__ void load_row(const T* p, float (&x)[E]) {
@@ -165,6 +163,71 @@ cudaError_t launch_t(const ServeArgs& a, int D, cudaStream_t s) {
   return note_error("cached decoding merge launch", cudaGetLastError());
 }
 
+// Joins the states of every query row: a warp a row.
+constexpr int kMergeWarps = 8;
+
+struct MergeParams {
+  ServeArgs a;
+  int tile, tile_rows, row_groups;  // of the pass over the own rows
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int E = D / 32;
+  const ServeArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int rows = a.group * a.nq;
+  const long long row = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= (long long)a.B * a.Hk * rows) return;
+  const long long slab = row / rows;
+  const int r = (int)(row - slab * rows), b = (int)(slab / a.Hk), hk = (int)(slab - (long long)b * a.Hk);
+  const int len = raw_len(a, b);
+  if (!len_ok(a, len)) return;
+  ptx::grid_wait();
+  float m = -INFINITY, mu = -INFINITY, l = 0.f, u[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) u[e] = 0.f;
+  auto join = [&](const float* pu, const float4* pml) {
+    const float4 s = *pml;
+    const float m_new = fmaxf(m, s.x), mu_new = fmaxf(mu, s.z);
+    l = l * join_factor(m, m_new) + s.y * join_factor(s.x, m_new);
+    const float f = join_factor(mu, mu_new), g = join_factor(s.z, mu_new);
+#pragma unroll
+    for (int e = 0; e < E; ++e) u[e] = u[e] * f + pu[lane * E + e] * g;
+    m = m_new;
+    mu = mu_new;
+  };
+  const int nt = own_tiles(len, p.tile);
+  if (nt > 0) {
+    const int rg = r / p.tile_rows;
+    const long long per = a.plan[0];
+    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * nt;
+    const long long c0 = t0 / per, c1 = (t0 + nt - 1) / per;
+    if (c0 == c1) {
+      join(a.row_u + row * D, a.row_ml + row);
+    } else {
+      for (long long c = c0; c <= c1; ++c) {
+        const long long at = (c * 2 + (c == c0 ? 1 : 0)) * p.tile_rows + (r - rg * p.tile_rows);
+        join(a.cut_u + at * D, a.cut_ml + at);
+      }
+    }
+  }
+  // l = 0: no key; NaN goes through
+  const float f = l == 0.f ? 0.f : exp2f(mu - m);
+#pragma unroll
+  for (int e = 0; e < E; ++e) st_elem(static_cast<T*>(a.o), row * D + lane * E + e, l == 0.f ? 0.f : u[e] / l * f);
+  if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <typename T>
+cudaError_t launch_merge(const MergeParams& p, int D, cudaStream_t s) {
+  const long long rows = (long long)p.a.B * p.a.Hk * p.a.group * p.a.nq;
+  const int ctas = (int)((rows + kMergeWarps - 1) / kMergeWarps);
+  return note_error("cached decoding merge launch",
+                    launch_serve_kernel(D == 64 ? merge_kernel<T, 64> : merge_kernel<T, 128>, ctas, kMergeWarps * 32, 0,
+                                        true, s, p));
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 DecodeSplit serve_split(int B, int Hk, long long keys) {
@@ -183,20 +246,64 @@ DecodeSplit serve_split(int B, int Hk, long long keys) {
 
 }  // namespace
 
+namespace {
+
+// Carves the workspace from `base`; returns the bytes taken.
+size_t carve(ServeArgs& a, int D, char* base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + at;
+    at += up256(bytes);
+    return p;
+  };
+  const size_t rows = (size_t)a.B * a.Hk * a.group * a.nq;
+  const size_t cut = (size_t)kOwnCtas * 2 * 16 * own_row_tiles(a.group * a.nq);
+  a.plan = reinterpret_cast<long long*>(take((size_t)(a.B + 1) * sizeof(long long)));
+  a.row_u = reinterpret_cast<float*>(take(rows * D * sizeof(float)));
+  a.row_ml = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
+  a.cut_u = reinterpret_cast<float*>(take(cut * D * sizeof(float)));
+  a.cut_ml = reinterpret_cast<float4*>(take(cut * sizeof(float4)));
+  return at;
+}
+
+}  // namespace
+
 size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, int D) {
-  const DecodeSplit sp = serve_split(B, Hk, (long long)np + max_len);
-  const size_t rows = (size_t)sp.splits * B * H * nq;
-  return up256(rows * D * sizeof(float)) + up256(rows * 2 * sizeof(float));
+  if (np > 0) {
+    const DecodeSplit sp = serve_split(B, Hk, (long long)np + max_len);
+    const size_t rows = (size_t)sp.splits * B * H * nq;
+    return up256(rows * D * sizeof(float)) + up256(rows * 2 * sizeof(float));
+  }
+  ServeArgs a{};
+  a.B = B;
+  a.Hk = Hk;
+  a.group = H / Hk;
+  a.nq = nq;
+  return carve(a, D, nullptr);
 }
 
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s) {
-  const DecodeSplit sp = serve_split(a.B, a.Hk, (long long)a.np + a.max_len);
-  a.splits = sp.splits;
-  a.keys_per_split = sp.keys_per_split;
-  const size_t rows = (size_t)sp.splits * a.B * a.Hk * a.group * a.nq;
-  a.part_u = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * D * sizeof(float)));
-  return dt == FA_F16 ? launch_t<__half>(a, D, s) : launch_t<__nv_bfloat16>(a, D, s);
+  if (a.np > 0) {
+    const DecodeSplit sp = serve_split(a.B, a.Hk, (long long)a.np + a.max_len);
+    a.splits = sp.splits;
+    a.keys_per_split = sp.keys_per_split;
+    const size_t rows = (size_t)sp.splits * a.B * a.Hk * a.group * a.nq;
+    a.part_u = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * D * sizeof(float)));
+    return dt == FA_F16 ? launch_t<__half>(a, D, s) : launch_t<__nv_bfloat16>(a, D, s);
+  }
+  carve(a, D, static_cast<char*>(workspace));
+  const int wr = own_row_tiles(a.group * a.nq);
+  MergeParams m;
+  m.tile = own_stage_keys(a.k_exp ? D : 2 * D) * (4 / wr);
+  m.tile_rows = 16 * wr;
+  m.row_groups = (a.group * a.nq + m.tile_rows - 1) / m.tile_rows;
+  if (a.max_len > 0) {
+    const cudaError_t e = a.k_exp ? launch_own_e4m3(a, D, dt == FA_F16, false, s) : launch_own_16(a, D, dt == FA_F16, false, s);
+    if (e != cudaSuccess) return e;
+  }
+  m.a = a;
+  return dt == FA_F16 ? launch_merge<__half>(m, D, s) : launch_merge<__nv_bfloat16>(m, D, s);
 }
 
 }  // namespace fa

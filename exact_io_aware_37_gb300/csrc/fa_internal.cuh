@@ -209,10 +209,20 @@ struct ServeArgs {
   float c2;             // scale * log2(e)
   int causal;
   unsigned* status;
+  unsigned long long wait_limit_ns;
+  // workspace: states of the own rows' units (fa_serve.cuh)
+  long long* plan;  // [1 + B]
+  float* row_u;     // [B * H * nq, D] units that one CTA covers
+  float4* row_ml;
+  float* cut_u;  // [2 * CTAs, rows of a CTA, D] the ends of the others
+  float4* cut_ml;
   float* part_u;
   float* part_ml;
   int splits, keys_per_split;
 };
+// The pass over the sequences' own rows, and the join of its states (np == 0).
+cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, bool after, cudaStream_t s);
+cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, bool after, cudaStream_t s);
 size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, int D);
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s);
 

@@ -1,0 +1,144 @@
+// What the kernels of a decoding step over a cache share: how the work is cut,
+// and where the states of the pieces lie in the workspace.
+//
+// A state of a query row over some keys is (m, l, mu, u): the weights' sum is
+// l 2^m and the weighted value sum u 2^mu (log2 units).
+#pragma once
+
+#include <math.h>
+
+#include "fa_internal.cuh"
+
+namespace fa {
+
+// CTAs of the pass over the own rows: two on each of 152 SMs.  Nothing depends on
+// how many run at once, and the workspace's size must not depend on the device.
+constexpr int kOwnCtas = 304;
+
+// Row tiles of 16 query rows in one CTA.
+inline int own_row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Keys of a stage of 4 KB.
+__host__ __device__ constexpr int own_stage_keys(int row_bytes) { return 4096 / row_bytes; }
+
+// A length out of range counts as 0 (the planner reports it, the merge skips it).
+__device__ __forceinline__ int raw_len(const ServeArgs& a, int b) { return a.lens ? __ldg(a.lens + b) : a.max_len; }
+__device__ __forceinline__ bool len_ok(const ServeArgs& a, int len) { return len >= 0 && len <= a.max_len; }
+__device__ __forceinline__ int seq_len(const ServeArgs& a, int b) {
+  const int len = raw_len(a, b);
+  return len_ok(a, len) ? len : 0;
+}
+__device__ __forceinline__ int own_tiles(int len, int tile) { return (int)(((unsigned)len + tile - 1) / tile); }
+
+// Factor of a state with maximum m joined under the maximum mm >= m: 1 for
+// equal maxima, -inf among them (that state holds nothing, or only NaN).
+__device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }
+
+// A CTA's run [first, end) of the tiles of all sequences laid out in a row
+// (sequence-major, units of a sequence, tiles of a unit); `base` tiles lie
+// before sequence b, which holds tile `first`.
+struct OwnPlan {
+  long long first, end, base, per_cta;
+  int b;
+};
+
+// Works out the CTA's run.  Block-wide; the caller's shared memory may be
+// initialised before it, since it ends with a block-wide barrier.  CTA 0 also
+// leaves the layout for the merge kernel: a.plan[0] = tiles a CTA, a.plan[1 + b] = tiles
+// before sequence b.
+template <int kThreads>
+__device__ __forceinline__ void own_plan(const ServeArgs& a, int tile, int units, OwnPlan& plan) {
+  __shared__ long long s_sum[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto tiles = [&](int b) -> long long {
+    if (b >= a.B) return 0;
+    const int len = raw_len(a, b);
+    if (!len_ok(a, len)) {
+      if (blockIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
+      return 0;
+    }
+    return (long long)own_tiles(len, tile) * units;
+  };
+  const long long mine = tiles(threadIdx.x);  // the first kThreads sequences: enough for most batches
+  long long x = mine;
+  for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) x += tiles(b);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  if (lane == 0) s_sum[warp] = x;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) total += s_sum[i];
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long first = min(total, per * blockIdx.x);
+  if (threadIdx.x == 0) {
+    plan.first = first;
+    plan.end = min(total, first + per);
+    plan.per_cta = per;
+    if (blockIdx.x == 0) a.plan[0] = per;
+  }
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const long long n = b0 == 0 ? mine : tiles(b);
+    long long incl = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += y;
+    }
+    __syncthreads();  // the last reads of s_sum
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long at = before + incl - n;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) at += s_sum[i];
+      before += s_sum[i];
+    }
+    if (b < a.B && at <= first && first < at + n) {
+      plan.base = at;
+      plan.b = b;
+    }
+    if (blockIdx.x == 0 && b < a.B) a.plan[1 + b] = at;
+  }
+  __syncthreads();
+}
+
+// Where a run's state goes: whole units to their rows' place, a unit's cut ends
+// to one of two places of the CTA (one for the part that continues a unit, one
+// for the part that begins it).
+struct PartSlot {
+  float* u;
+  float4* ml;  // (m, l, mu, unused)
+};
+__device__ __forceinline__ PartSlot own_slot(const ServeArgs& a, int cta, bool begins, bool ends, int slab, int row0,
+                                             int tile_rows, int rows, int D) {
+  if (begins && ends) {
+    const long long r = (long long)slab * rows + row0;
+    return PartSlot{a.row_u + r * D, a.row_ml + r};
+  }
+  const long long r = ((long long)cta * 2 + (begins ? 1 : 0)) * tile_rows;
+  return PartSlot{a.cut_u + r * D, a.cut_ml + r};
+}
+
+// Launches a kernel that takes its parameters by value; `after`: it may start
+// before the kernel in front of it has finished (and waits for it with
+// grid_wait where it needs its results).
+template <typename P>
+cudaError_t launch_serve_kernel(void (*kernel)(P), int ctas, int threads, int smem, bool after, cudaStream_t s,
+                                const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  note_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace fa

@@ -132,7 +132,7 @@ def test_decode_exponents_and_prefix_pointers(lib):
     assert _shared(lib, ke=P) == INVALID and _shared(lib, ve=P) == INVALID      # one without the other
     assert _shared(lib, kp=None) == INVALID and _shared(lib, vp=P + 8) == ALIGN
     assert _shared(lib, np=-1) == INVALID
-    assert _shared(lib, np=(1 << 31) - 100, cap=512) == UNSUPPORTED
+    assert _shared(lib, np=(1 << 30) - 400, cap=512) == UNSUPPORTED
 
 
 def test_workspace_sizes(lib):
