@@ -23,17 +23,18 @@ LIB_PATH = os.path.join(BUILD, LIB_NAME)
 
 SOURCES = ["fa_api.cu", "fa_simt.cu", "fa_tc_fwd.cu", "fa_tc_bwd.cu", "fa_tc_bwd128.cu", "fa_static_ws.cu",
            "fa_decode.cu", "fa_tc_bwd_dq.cu", "fa_probe.cu", "fa_selftest.cu", "fa_cache8.cu", "fa_decode_cache.cu",
-           "fa_serve_own8.cu", "fa_serve_own16.cu"]
+           "fa_serve_own8.cu", "fa_serve_own16.cu", "fa_tc_prefix.cu"]
 
 # The tensor-core kernels move registers between warpgroups with setmaxnreg
 # (384-thread kernels from 168 registers per thread at launch: the forward
-# 200 + 200 + 104, the backward 184 + 184 + 136).  Each split is only safe
+# 200 + 200 + 104, as the shared prefix's, the backward 184 + 184 + 136).  Each split is only safe
 # when every thread starts with the launch count it was sized for; a kernel
 # that ptxas compiled with fewer would wait forever in setmaxnreg.inc, so the
 # build refuses it.
 # kernel name -> registers per thread it must be compiled with (checked in order)
-SPLIT_KERNELS = {"tc_bwd128_kernel": 168, "tc_fwd_kernel": 168, "tc_bwd_dq_kernel": 168}
-SPLIT_SOURCES = ("fa_tc_fwd.cu", "fa_tc_bwd128.cu", "fa_tc_bwd_dq.cu")  # each must report its split kernels
+SPLIT_KERNELS = {"tc_bwd128_kernel": 168, "tc_fwd_kernel": 168, "tc_bwd_dq_kernel": 168, "tc_prefix_kernel": 168}
+# each must report its split kernels
+SPLIT_SOURCES = ("fa_tc_fwd.cu", "fa_tc_bwd128.cu", "fa_tc_bwd_dq.cu", "fa_tc_prefix.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC]

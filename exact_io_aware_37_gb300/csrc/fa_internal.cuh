@@ -216,11 +216,12 @@ struct ServeArgs {
   float4* row_ml;
   float* cut_u;  // [2 * CTAs, rows of a CTA, D] the ends of the others
   float4* cut_ml;
-  float* part_u;
-  float* part_ml;
-  int splits, keys_per_split;
+  float* pre_u;  // [parts of all units, 2 slots, rows of a slot, D] the prefix's states
+  float4* pre_ml;
 };
-// The pass over the sequences' own rows, and the join of its states (np == 0).
+struct PrefixPlan;
+cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, cudaStream_t s);
+// The pass over the sequences' own rows; `after`: in the prefix's wake.
 cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, bool after, cudaStream_t s);
 cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, bool after, cudaStream_t s);
 size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, int D);

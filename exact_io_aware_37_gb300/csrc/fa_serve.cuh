@@ -121,6 +121,35 @@ __device__ __forceinline__ PartSlot own_slot(const ServeArgs& a, int cta, bool b
   return PartSlot{a.cut_u + r * D, a.cut_ml + r};
 }
 
+// The pass over the prefix (fa_tc_prefix.cu): units of kPrefixRows (split) or
+// 2 kPrefixRows query rows of a key head, each of `steps` tiles of kPrefixKeys keys;
+// all units' steps in a row, per_cta of them a CTA.
+constexpr int kPrefixRows = 128, kPrefixKeys = 128;
+constexpr int kPrefixCtas = 152;  // one an SM; a constant for the workspace's sake, as above
+struct PrefixPlan {
+  int split;              // at most kPrefixRows rows: the two slots share them and halve the keys
+  int pairs, steps, units;
+  int ctas, parts;        // parts: states kept for a unit (CTAs that may share it)
+  long long per_cta;
+};
+inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np) {
+  PrefixPlan p;
+  const long long rows = (long long)B * gq;
+  p.split = rows <= kPrefixRows;
+  p.pairs = (int)((rows + 2 * kPrefixRows - 1) / (2 * kPrefixRows));
+  p.steps = (np + kPrefixKeys - 1) / kPrefixKeys;
+  p.units = p.pairs * Hk;
+  const long long all = (long long)p.units * p.steps;
+  p.per_cta = (all + kPrefixCtas - 1) / kPrefixCtas;
+  p.ctas = p.per_cta > 0 ? (int)((all + p.per_cta - 1) / p.per_cta) : 0;
+  p.parts = p.per_cta > 0 ? (int)((p.steps - 1) / p.per_cta) + 2 : 0;
+  return p;
+}
+// The state's place of a unit's part that CTA `cta` works on.
+__device__ __forceinline__ int prefix_part(const PrefixPlan& p, int unit, int cta) {
+  return unit * p.parts + (cta - (int)((long long)unit * p.steps / p.per_cta));
+}
+
 // Launches a kernel that takes its parameters by value; `after`: it may start
 // before the kernel in front of it has finished (and waits for it with
 // grid_wait where it needs its results).

@@ -373,6 +373,18 @@ __device__ __forceinline__ void mma_ts_x8(uint32_t d, const uint32_t (&a)[8], co
       : "memory");
 }
 
+__device__ __forceinline__ void mma_ts_x4(uint32_t d, const uint32_t (&a)[4], const uint64_t (&b)[4], uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %9, 0;\n setp.eq.b32 q, %9, %9;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %10, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %10, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %10, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %10, q;\n}\n" ::"r"(d),
+      "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "r"(acc), "r"(idesc)
+      : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
