@@ -36,15 +36,20 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;  // false for NaN too
 }
 
-// Two scaled values to two codes (round to nearest even), `lo` in the low
-// byte.  The conversion saturates, so an infinity is turned into NaN first.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-  lo = fabsf(lo) < INFINITY ? lo : __uint_as_float(0x7fffffffu);
-  hi = fabsf(hi) < INFINITY ? hi : __uint_as_float(0x7fffffffu);
+// Two values of magnitude at most 448, or NaN, to two codes (round to nearest
+// even), `lo` in the low byte.
+__device__ __forceinline__ uint32_t encode2_finite(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The same with infinities, which the conversion would saturate, to NaN.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  lo = fabsf(lo) < INFINITY ? lo : __uint_as_float(0x7fffffffu);
+  hi = fabsf(hi) < INFINITY ? hi : __uint_as_float(0x7fffffffu);
+  return encode2_finite(lo, hi);
+}
+
 // Two codes (low 16 bits of u) to an fp16 pair, exactly.
 __device__ __forceinline__ uint32_t decode2_f16(uint32_t u) {
   uint32_t r;
@@ -54,6 +59,19 @@ __device__ __forceinline__ uint32_t decode2_f16(uint32_t u) {
 __device__ __forceinline__ float2 decode2(uint32_t u) {
   const uint32_t h = decode2_f16(u);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Two values (at most 448 each) as sums of three codes each, x = c0 + c1 / 16 +
+// c2 / 256: 4 bits a term, 12 in all, down to 2^-18 absolute (half of c2's smallest
+// step, 2^-9 / 256).
+__device__ __forceinline__ void encode2_terms(float lo, float hi, uint32_t (&t)[3]) {
+  t[0] = encode2_finite(lo, hi);
+  float2 c = decode2(t[0]);
+  lo = (lo - c.x) * 16.f;
+  hi = (hi - c.y) * 16.f;
+  t[1] = encode2_finite(lo, hi);
+  c = decode2(t[1]);
+  t[2] = encode2_finite((lo - c.x) * 16.f, (hi - c.y) * 16.f);
 }
 
 }  // namespace c8

@@ -24,7 +24,7 @@ constexpr int kMergeWarps = 8;
 
 struct MergeParams {
   ServeArgs a;
-  int tile, tile_rows, row_groups;  // of the pass over the own rows
+  int cta_rows, row_groups;  // of the pass over the own rows
   PrefixPlan pre;
 };
 
@@ -67,9 +67,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
       if (p.pre.split) join(a.pre_u + (at + kPrefixRows) * D, a.pre_ml + at + kPrefixRows);
     }
   }
-  const int nt = own_tiles(len, p.tile);
+  const int nt = own_tiles(len, kOwnTile);
   if (nt > 0) {
-    const int rg = r / p.tile_rows;
+    const int rg = r / p.cta_rows;
     const long long per = a.plan[0];
     const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * nt;
     const long long c0 = t0 / per, c1 = (t0 + nt - 1) / per;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
       join(a.row_u + row * D, a.row_ml + row);
     } else {
       for (long long c = c0; c <= c1; ++c) {
-        const long long at = (c * 2 + (c == c0 ? 1 : 0)) * p.tile_rows + (r - rg * p.tile_rows);
+        const long long at = (c * 2 + (c == c0 ? 1 : 0)) * p.cta_rows + (r - rg * p.cta_rows);
         join(a.cut_u + at * D, a.cut_ml + at);
       }
     }
@@ -109,7 +109,7 @@ size_t carve(ServeArgs& a, int D, const PrefixPlan& pre, char* base) {
     return p;
   };
   const size_t rows = (size_t)a.B * a.Hk * a.group * a.nq;
-  const size_t cut = (size_t)kOwnCtas * 2 * 16 * own_row_tiles(a.group * a.nq);
+  const size_t cut = (size_t)kOwnCtas * 2 * own_rows(a.group * a.nq);
   if (a.np > 0) {
     const size_t states = (size_t)pre.units * pre.parts * 2 * kPrefixRows;
     a.pre_u = reinterpret_cast<float*>(take(states * D * sizeof(float)));
@@ -139,11 +139,9 @@ size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, 
 
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s) {
   const bool f16 = dt == FA_F16;
-  const int wr = own_row_tiles(a.group * a.nq);
   MergeParams m;
-  m.tile = own_stage_keys(a.k_exp ? D : 2 * D) * (4 / wr);
-  m.tile_rows = 16 * wr;
-  m.row_groups = (a.group * a.nq + m.tile_rows - 1) / m.tile_rows;
+  m.cta_rows = own_rows(a.group * a.nq);
+  m.row_groups = (a.group * a.nq + m.cta_rows - 1) / m.cta_rows;
   m.pre = prefix_plan(a.B, a.Hk, a.group * a.nq, a.np);
   carve(a, D, m.pre, static_cast<char*>(workspace));
   cudaError_t e = cudaSuccess;

@@ -11,14 +11,15 @@
 
 namespace fa {
 
-// CTAs of the pass over the own rows: two on each of 152 SMs.  Nothing depends on
-// how many run at once, and the workspace's size must not depend on the device.
+// The pass over the own rows (fa_serve_own.cuh): at most two CTAs on each of 152
+// SMs.  Nothing depends on how many run at once, and the workspace's size must not
+// depend on the device.
 constexpr int kOwnCtas = 304;
-
-// Row tiles of 16 query rows in one CTA.
-inline int own_row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-// Keys of a stage of 4 KB.
-__host__ __device__ constexpr int own_stage_keys(int row_bytes) { return 4096 / row_bytes; }
+constexpr int kOwnTile = 128;  // keys of a step
+// Query rows of a CTA: what the rows of a key head fill, so that fewer rows leave fewer
+// columns to multiply and read out.  More than 32 are spread over row groups, which
+// read the same keys at about the same time, so mostly from L2.
+inline int own_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // A length out of range counts as 0 (the planner reports it, the merge skips it).
 __device__ __forceinline__ int raw_len(const ServeArgs& a, int b) { return a.lens ? __ldg(a.lens + b) : a.max_len; }
@@ -111,13 +112,10 @@ struct PartSlot {
   float* u;
   float4* ml;  // (m, l, mu, unused)
 };
-__device__ __forceinline__ PartSlot own_slot(const ServeArgs& a, int cta, bool begins, bool ends, int slab, int row0,
-                                             int tile_rows, int rows, int D) {
-  if (begins && ends) {
-    const long long r = (long long)slab * rows + row0;
-    return PartSlot{a.row_u + r * D, a.row_ml + r};
-  }
-  const long long r = ((long long)cta * 2 + (begins ? 1 : 0)) * tile_rows;
+__device__ __forceinline__ PartSlot own_slot(const ServeArgs& a, int cta, bool begins, bool ends, long long row,
+                                             int cta_rows, int D) {
+  if (begins && ends) return PartSlot{a.row_u + row * D, a.row_ml + row};
+  const long long r = ((long long)cta * 2 + (begins ? 1 : 0)) * cta_rows;
   return PartSlot{a.cut_u + r * D, a.cut_ml + r};
 }
 

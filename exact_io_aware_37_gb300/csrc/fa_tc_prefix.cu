@@ -101,7 +101,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     return true;
   };
 
-  grid_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(&bar_k0, 1);
     mbar_init(&bar_done, 1);
@@ -125,6 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // not before the allocation: a kernel started early may take tensor memory too
+  grid_launch_dependents();
   const uint32_t tmem = tmem_base_sh;
   const WaitCtx w{&abort_flag, a.status, a.wait_limit_ns};
 
