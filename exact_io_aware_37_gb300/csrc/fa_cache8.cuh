@@ -61,17 +61,24 @@ __device__ __forceinline__ float2 decode2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Two values (at most 448 each) as sums of three codes each, x = c0 + c1 / 16 +
-// c2 / 256: 4 bits a term, 12 in all, down to 2^-18 absolute (half of c2's smallest
-// step, 2^-9 / 256).
-__device__ __forceinline__ void encode2_terms(float lo, float hi, uint32_t (&t)[3]) {
-  t[0] = encode2_finite(lo, hi);
-  float2 c = decode2(t[0]);
-  lo = (lo - c.x) * 16.f;
-  hi = (hi - c.y) * 16.f;
-  t[1] = encode2_finite(lo, hi);
-  c = decode2(t[1]);
-  t[2] = encode2_finite((lo - c.x) * 16.f, (hi - c.y) * 16.f);
+// Two fp16 values (at most 448 each, or NaN) as sums of three codes each, x = c0 +
+// c1 / 16 + c2 / 256: 4 bits a term, 12 in all (fp16 has 11), down to 2^-18 absolute
+// (half of c2's smallest step, 2^-9 / 256).  Every difference is exact in fp16.
+__device__ __forceinline__ uint32_t encode2_f16(__half2 h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+  return r;
+}
+__device__ __forceinline__ void encode2_terms(__half2 h, uint32_t (&t)[3]) {
+  const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    t[k] = encode2_f16(h);
+    if (k < 2) {
+      const uint32_t c = decode2_f16(t[k]);
+      h = __hfma2(*reinterpret_cast<const __half2*>(&c), down, __hmul2(h, up));
+    }
+  }
 }
 
 }  // namespace c8

@@ -67,11 +67,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
       if (p.pre.split) join(a.pre_u + (at + kPrefixRows) * D, a.pre_ml + at + kPrefixRows);
     }
   }
-  const int nt = own_tiles(len, kOwnTile);
+  const int nt = own_tiles(len);
   if (nt > 0) {
     const int rg = r / p.cta_rows;
     const long long per = a.plan[0];
-    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * nt;
+    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * own_cost(nt) + kRunCost;
     const long long c0 = t0 / per, c1 = (t0 + nt - 1) / per;
     if (c0 == c1) {
       join(a.row_u + row * D, a.row_ml + row);

@@ -16,10 +16,17 @@ namespace fa {
 // depend on the device.
 constexpr int kOwnCtas = 304;
 constexpr int kOwnTile = 128;  // keys of a step
+// What a run costs besides its tiles (queries in, references found, state out), in tiles: it
+// only steers the cut.  Measured on 32 ragged sequences of 4 to 2048 keys, 32 key heads: without it the CTAs
+// that got the short sequences took twice the average.
+constexpr int kRunCost = 2;
 // Query rows of a CTA: what the rows of a key head fill, so that fewer rows leave fewer
-// columns to multiply and read out.  More than 32 are spread over row groups, which
+// columns to multiply and read out.  More than 24 are spread over row groups, which
 // read the same keys at about the same time, so mostly from L2.
-inline int own_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+inline int own_rows(int rows) {
+  if (rows <= 16) return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+  return (rows + 15) / 16 * 16 <= (rows + 23) / 24 * 24 ? 16 : 24;  // the one that pads less
+}
 
 // A length out of range counts as 0 (the planner reports it, the merge skips it).
 __device__ __forceinline__ int raw_len(const ServeArgs& a, int b) { return a.lens ? __ldg(a.lens + b) : a.max_len; }
@@ -28,40 +35,43 @@ __device__ __forceinline__ int seq_len(const ServeArgs& a, int b) {
   const int len = raw_len(a, b);
   return len_ok(a, len) ? len : 0;
 }
-__device__ __forceinline__ int own_tiles(int len, int tile) { return (int)(((unsigned)len + tile - 1) / tile); }
+__device__ __forceinline__ int own_tiles(int len) { return (int)(((unsigned)len + kOwnTile - 1) / kOwnTile); }
+// Cost of a unit of `tiles` tiles: the run's own cost, then a tile each.
+__device__ __forceinline__ int own_cost(int tiles) { return tiles > 0 ? tiles + kRunCost : 0; }
 
 // Factor of a state with maximum m joined under the maximum mm >= m: 1 for
 // equal maxima, -inf among them (that state holds nothing, or only NaN).
 __device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }
 
-// A CTA's run [first, end) of the tiles of all sequences laid out in a row
-// (sequence-major, units of a sequence, tiles of a unit); `base` tiles lie
-// before sequence b, which holds tile `first`.
+// A CTA's share [first, end) of the cost of all sequences laid out in a row
+// (sequence-major, units of a sequence, in a unit kRunCost and then its tiles); `base`
+// lies before sequence b, which holds position `first`.  A tile belongs to the CTA whose
+// share its position falls into.
 struct OwnPlan {
-  long long first, end, base, per_cta;
+  long long first, end, base;
   int b;
 };
 
-// Works out the CTA's run.  Block-wide; the caller's shared memory may be
+// Works out the CTA's share.  Block-wide; the caller's shared memory may be
 // initialised before it, since it ends with a block-wide barrier.  CTA 0 also
-// leaves the layout for the merge kernel: a.plan[0] = tiles a CTA, a.plan[1 + b] = tiles
-// before sequence b.
+// leaves the layout for the merge kernel: a.plan[0] = a CTA's share, a.plan[1 + b] = what
+// lies before sequence b.
 template <int kThreads>
-__device__ __forceinline__ void own_plan(const ServeArgs& a, int tile, int units, OwnPlan& plan) {
+__device__ __forceinline__ void own_plan(const ServeArgs& a, int units, OwnPlan& plan) {
   __shared__ long long s_sum[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto tiles = [&](int b) -> long long {
+  auto cost = [&](int b) -> long long {
     if (b >= a.B) return 0;
     const int len = raw_len(a, b);
     if (!len_ok(a, len)) {
       if (blockIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
       return 0;
     }
-    return (long long)own_tiles(len, tile) * units;
+    return (long long)own_cost(own_tiles(len)) * units;
   };
-  const long long mine = tiles(threadIdx.x);  // the first kThreads sequences: enough for most batches
+  const long long mine = cost(threadIdx.x);  // the first kThreads sequences: enough for most batches
   long long x = mine;
-  for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) x += tiles(b);
+  for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) x += cost(b);
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
   if (lane == 0) s_sum[warp] = x;
@@ -74,13 +84,12 @@ __device__ __forceinline__ void own_plan(const ServeArgs& a, int tile, int units
   if (threadIdx.x == 0) {
     plan.first = first;
     plan.end = min(total, first + per);
-    plan.per_cta = per;
     if (blockIdx.x == 0) a.plan[0] = per;
   }
   long long before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const long long n = b0 == 0 ? mine : tiles(b);
+    const long long n = b0 == 0 ? mine : cost(b);
     long long incl = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {

@@ -22,16 +22,16 @@
 // by warp-level MMA were tried first: about 60 cycles each a warp on this part, so eight
 // warps an SM held the step at 239 us, B16 H32 8192 keys D128, floor 159.)
 //
-// Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread: a tile's
-// references hold unless some score outgrows them, which one barrier with a vote
-// finds out; the threads write P^T as the second product's narrow operand, one byte (or 16-bit
-// value) a row and term, and read O^T at a run's end.  Warp 4: TMA producer, rings
-// of K and V tiles that run on over a CTA's runs.  Warp 5: MMA issuer; S^T of the
-// next tile is issued before the softmax of this one is done.
+// Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile's
+// references hold unless some score outgrows them, which a first look at the scores and one barrier with
+// a vote find out; the threads write P^T as the second product's narrow operand, one byte
+// (or 16-bit value) a row and term, and read O^T at a run's end, by when the next run's queries are in
+// place.  Warp 4: TMA producer; K and V tiles share one ring that runs on over a CTA's
+// runs.  Warp 5: MMA issuer; S^T of the next tile is issued before the softmax of this one is done.
 //
 // Schedule.  The tiles of all (sequence, head, row group) units are laid out in
-// a row and cut into equal runs, one a CTA, from the lengths on the device;
-// a unit that is cut leaves one state a run, joined by the merge kernel.
+// a row and cut into equal shares, one a CTA, from the lengths on the device; a run is
+// what a share holds of one unit.  A unit that is cut leaves one state a run, joined by the merge kernel.
 #pragma once
 
 #include <math.h>
@@ -52,7 +52,7 @@ constexpr int kOwnTmaWarp = 4, kOwnMmaWarp = 5;
 constexpr int kBoxKeys = 32;  // keys of one TMA box: a last tile reads no more boxes than it has keys for
 // Weights are rounded relative to 2^-7 (codes): at most 2 by the reference's rule, so
 // at most 256 of e4m3's 448, and the terms reach down to 2^-18 / 2^7 = 2^-25, as fp16 does.
-constexpr float kWeightScale = 128.f;
+constexpr float kWeightLog2 = 7.f;
 constexpr float kRefSlack = 1.f;    // log2 units a weight may outgrow its reference by
 constexpr float kSumSlack = 60.f;   // the same for the float32 normaliser
 
@@ -80,18 +80,19 @@ struct OwnCfg {
   static constexpr int kPRow = kOwnTile * kElem;          // P^T: a row's 128 weights
   static constexpr int kPBlocks = kPRow / 128;
   static constexpr int kPBlock = kN * 128;
-  // V in front of K: at D = 64 the second half of the 128 rows of V^T is read from what follows V
-  // (its products go to tensor-memory lanes that nothing reads)
-  static constexpr int kStageBytes = 2 * kTileBytes;
-  // as many stages as leave room for a second CTA on the SM, where two fit at all
-  static constexpr int kNarrow = (kPBlocks * kPBlock + 1023) / 1024 * 1024 + (kBlocks * kQBlock + 1023) / 1024 * 1024;
-  static constexpr int kStages = kStageBytes > 32768 ? 3 : (110 * 1024 - kNarrow) / kStageBytes;
-  static constexpr int kPOff = kStages * kStageBytes;
-  static constexpr int kQOff = kPOff + (kPBlocks * kPBlock + 1023) / 1024 * 1024;
-  static constexpr int kSmem = kQOff + (kBlocks * kQBlock + 1023) / 1024 * 1024 + 1024;
-  static constexpr int kPerSm = kSmem <= 112 * 1024 ? 2 : 1;
-  static constexpr int kCols = 2 * kN <= 32 ? 32 : 2 * kN <= 64 ? 64 : 2 * kN <= 128 ? 128 : 256;  // S^T, O^T
-  static constexpr int kChunk = R < 8 || R == 32 ? 4 : 8;  // rows read out together (32: four, for the registers' sake)
+  static constexpr int kPOff = 0;
+  static constexpr int kQOff = (kPBlocks * kPBlock + 1023) / 1024 * 1024;
+  static constexpr int kRingOff = kQOff + (kBlocks * kQBlock + 1023) / 1024 * 1024;
+  // at D = 64 the second half of V^T's 128 rows is read from what follows V (its products go to
+  // tensor-memory lanes that nothing reads); past the ring's last slot that is this many bytes
+  static constexpr int kPad = D == 64 ? kTileBytes : 0;
+  // as many slots as leave room for a second CTA on the SM, if that is three
+  static constexpr int kFit = (110 * 1024 - kRingOff - kPad) / kTileBytes;
+  static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
+  static constexpr int kSlots = kFit >= 3 ? (kFit < 8 ? kFit : 8) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
+  static constexpr int kSmem = kRingOff + kSlots * kTileBytes + kPad + 1024;
+  static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;  // two S^T, O^T
+  static constexpr int kChunk = R < 8 ? R : 8;                                 // rows read out together
 };
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block.
@@ -126,23 +127,34 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
+// What the threads share about a query row of a run.
+struct RowInfo {
+  float factor;      // from products to log2 units
+  float neg_w, neg_l;  // minus the references (0 without a key so far; neg_w holds the weights' scale)
+  int limit;         // keys it sees
+};
+
 template <int Kind, int D, int R>
 __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_kernel(
     const __grid_constant__ OwnParams p) {
   using C = OwnCfg<Kind, D, R>;
-  constexpr int S = C::kStages;
+  constexpr unsigned H = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // Steps (tiles) g are counted over all of a CTA's runs.  full / free: rings of K and V;
-  // bar_s: S^T(g) complete; bar_sfree: read out; bar_p: P^T(g) written; bar_o: O^T += (g)
+  // Steps (tiles) g are counted over all of a CTA's runs.  full / free: the ring; bar_s[g % 2]:
+  // S^T(g) complete; bar_sfree[g % 2]: read out; bar_p: P^T(g) written; bar_o: O^T += (g)
   // complete; bar_q: a run's Q written.
-  __shared__ __align__(8) uint64_t bar_fullk[S], bar_fullv[S], bar_freek[S], bar_freev[S];
-  __shared__ __align__(8) uint64_t bar_s, bar_sfree, bar_p, bar_o, bar_q, bar_done;
-  __shared__ float s_rs[R], s_refw[R], s_refl[R], s_alw[R], s_all[R];  // row factor, references, rescaling
-  __shared__ float s_mw[4][R], s_ml[4][R];                              // warps' maxima; sums at a run's end
+  __shared__ __align__(8) uint64_t bar_full[H], bar_free[H];
+  __shared__ __align__(8) uint64_t bar_s[2], bar_sfree[2], bar_p, bar_o, bar_q, bar_done;
+  // by the run's parity: the next run's are written while this one's are in use
+  __shared__ __align__(16) RowInfo s_row[2][R];
+  __shared__ float s_refw[2][R], s_refl[2][R];  // references of the weights and of the normaliser
+  __shared__ float s_mw[4][R], s_ml[4][R];      // warps' maxima, and sums at a run's end
+  __shared__ float s_fw[R], s_fl[R];            // rescaling
+  __shared__ int s_bad[2];
   __shared__ OwnPlan plan;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag, s_bad;
+  __shared__ int abort_flag;
 
   const ServeArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,14 +162,14 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   const int units = a.Hk * p.row_groups;  // of one sequence
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&bar_fullk[s], 1);
-      mbar_init(&bar_fullv[s], 1);
-      mbar_init(&bar_freek[s], 1);
-      mbar_init(&bar_freev[s], 1);
+    for (unsigned s = 0; s < H; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_free[s], 1);
     }
-    mbar_init(&bar_s, 1);
-    mbar_init(&bar_sfree, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar_s[s], 1);
+      mbar_init(&bar_sfree[s], 4);
+    }
     mbar_init(&bar_p, 4);
     mbar_init(&bar_o, 1);
     mbar_init(&bar_q, 4);
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     tmem_relinquish();
   }
   tc_fence_before();
-  own_plan<kOwnThreads>(a, kOwnTile, units, plan);  // holds block-wide barriers
+  own_plan<kOwnThreads>(a, units, plan);  // holds block-wide barriers
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem = tmem_base_sh;
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 
   // ---- the CTA's runs, walked alike by every role
   struct Run {
-    int b, len, hk, row0, slab, tile0, n;
+    int b, len, row0, slab, tile0, n;
     bool ends;  // the run holds the unit's last tile
   };
   struct Walk {
@@ -188,122 +200,150 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     int b;
   };
   auto next_run = [&](Walk& k, Run& q) -> bool {
-    if (k.t >= plan.end) return false;
-    for (;;) {
+    while (k.t < plan.end) {
       q.len = seq_len(a, k.b);
-      const int nt = own_tiles(q.len, kOwnTile);
-      const long long here = (long long)nt * units;
-      if (k.t < k.base + here) {
-        const long long at = k.t - k.base;
-        const int unit = (int)(at / nt);
-        q.tile0 = (int)(at - (long long)unit * nt);
-        q.n = (int)min((long long)(nt - q.tile0), plan.end - k.t);
-        q.ends = q.tile0 + q.n == nt;
-        q.b = k.b;
-        q.hk = unit / p.row_groups;
-        q.row0 = (unit - q.hk * p.row_groups) * R;
-        q.slab = k.b * a.Hk + q.hk;
-        k.t += q.n;
-        return true;
+      const int nt = own_tiles(q.len), cost = own_cost(nt);
+      const long long here = (long long)cost * units;
+      if (k.t >= k.base + here) {
+        k.base += here;
+        ++k.b;
+        continue;
       }
-      k.base += here;
-      ++k.b;
+      const long long at = k.t - k.base;
+      const int unit = (int)(at / cost);
+      const int x0 = (int)(at - (long long)unit * cost);
+      const int x1 = (int)min((long long)cost, x0 + (plan.end - k.t));
+      k.t += x1 - x0;
+      q.tile0 = max(0, x0 - kRunCost);
+      q.n = max(0, x1 - kRunCost) - q.tile0;
+      if (q.n <= 0) continue;  // the share ends before the unit's first tile
+      q.ends = x1 == cost;
+      q.b = k.b;
+      const int hk = unit / p.row_groups;
+      q.row0 = (unit - hk * p.row_groups) * R;
+      q.slab = k.b * a.Hk + hk;
+      return true;
     }
+    return false;
   };
   Walk walk{plan.first, plan.base, plan.b};
-  Run q;
 
   if (warp < 4) {
     // ------------------------------------------------------------ softmax
     const int tid = threadIdx.x;  // the key of a tile that this thread holds
     const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t t_o = t_s + C::kN;
+    const uint32_t t_o = t_s + 2 * C::kN;
     uint8_t* sp = smem + C::kPOff;
     uint8_t* sq = smem + C::kQOff;
-    bool ok = true;
-    unsigned g = 0;
-    while (ok && next_run(walk, q)) {
+    constexpr int kRowThreads = D / 8;  // threads of a query row, 8 elements each
+    constexpr int kPass = 128 / kRowThreads, kPasses = (R + kPass - 1) / kPass;
+    const int qr = tid / kRowThreads, qx = tid % kRowThreads * 8;
+
+    // ---- a run's queries: loaded early, put in place later
+    uint4 qv[kPasses];
+    auto load_q = [&](const Run& q) {
       const int valid = min(R, rows - q.row0);
-      const long long row_at = (long long)q.slab * rows + q.row0;  // of q, o and the states
-      // ---- the run's queries: the narrow operand of S^T (the previous run's products are complete)
-      if constexpr (C::kCodes) {
-        constexpr int kLanes = D / 8;  // threads of a row, 8 elements each
-        for (int r0 = 0; r0 < R; r0 += 128 / kLanes) {
-          const int r = r0 + tid / kLanes, x0 = tid % kLanes * 8;
-          float x[8];
-          if (r < valid) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (row_at + r) * D + x0);
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = p.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[e]))
-                                       : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v[e]));
-              x[2 * e] = f.x;
-              x[2 * e + 1] = f.y;
-            }
-          } else {
+      for (int x = 0; x < kPasses; ++x) {
+        const int r = x * kPass + qr;
+        qv[x] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                            ((long long)q.slab * rows + q.row0 + r) * D + qx)
+                          : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // The narrow operand of S^T and what the rows' threads share; every S^T of the run before is complete.
+    auto put_q = [&](const Run& q, int par) {
+      const int valid = min(R, rows - q.row0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-          }
-          float big = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) big = fmaxf(big, c8::finite_abs(x[e]));
-#pragma unroll
-          for (int m = kLanes / 2; m >= 1; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
-          const int eb = c8::exp_byte(big);
-          const float f = c8::inv_scale(eb);
-          uint32_t t[3][4];
+      for (int x = 0; x < kPasses; ++x) {
+        const int r = x * kPass + qr;
+        float factor = a.c2;
+        if constexpr (C::kCodes) {
+          const uint32_t v[4] = {qv[x].x, qv[x].y, qv[x].z, qv[x].w};
+          float f[8], big = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float lo = x[2 * e] * f, hi = x[2 * e + 1] * f;
+            const float2 y = p.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[e]))
+                                     : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v[e]));
+            f[2 * e] = y.x;
+            f[2 * e + 1] = y.y;
+            big = fmaxf(big, fmaxf(c8::finite_abs(y.x), c8::finite_abs(y.y)));
+          }
+#pragma unroll
+          for (int m = kRowThreads / 2; m >= 1; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+          // scaled by a power of two to at most 448: exact in fp16 but for elements below
+          // 2^-14 / 448 of the row's largest (infinities become NaN)
+          const int eb = c8::exp_byte(big);
+          const float scale = c8::inv_scale(eb);
+          factor *= c8::scale(eb);
+          uint32_t t[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float lo = f[2 * e] * scale, hi = f[2 * e + 1] * scale;
             lo = fabsf(lo) < INFINITY ? lo : __uint_as_float(0x7fffffffu);
             hi = fabsf(hi) < INFINITY ? hi : __uint_as_float(0x7fffffffu);
-            uint32_t y[3];
-            c8::encode2_terms(lo, hi, y);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) t[k][e] = y[k];
+            c8::encode2_terms(__floats2half2_rn(lo, hi), t[e]);
           }
-          if (r < R) {
+          if (r < R)
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const int row = k * R + r;
-              *reinterpret_cast<uint2*>(sq + swz<C::kPitch>(row, x0 >> 4) + (x0 & 15)) =
-                  make_uint2(t[k][0] | t[k][1] << 16, t[k][2] | t[k][3] << 16);
-            }
-            if (x0 == 0) s_rs[r] = a.c2 * c8::scale(eb);
-          }
+            for (int k = 0; k < 3; ++k)
+              *reinterpret_cast<uint2*>(sq + swz<C::kPitch>(k * R + r, qx >> 4) + (qx & 15)) =
+                  make_uint2(t[0][k] | t[1][k] << 16, t[2][k] | t[3][k] << 16);
+        } else if (r < R) {
+          *reinterpret_cast<uint4*>(sq + (qx >> 6) * C::kQBlock + swz<C::kPitch>(r, (qx & 63) >> 3)) = qv[x];
         }
-      } else {
-        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-        for (int i = tid; i < R * kChunks; i += 128) {
-          const int r = i / kChunks, ch = i % kChunks;
-          const uint4 u = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                      (row_at + r) * D + ch * 8)
-                                    : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sq + (ch >> 3) * C::kQBlock + swz<C::kPitch>(r, ch & 7)) = u;
+        if (r < R && qx == 0) {
+          // a row past the last weighs nothing and outgrows nothing
+          const bool there = r < valid;
+          s_row[par][r] = RowInfo{factor, there ? 0.f : -INFINITY, there ? 0.f : -INFINITY,
+                                  a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len};
+          s_refw[par][r] = s_refl[par][r] = there ? -INFINITY : INFINITY;
         }
-        if (tid < R) s_rs[tid] = a.c2;
       }
-      if (tid < R) s_refw[tid] = s_refl[tid] = tid < valid ? -INFINITY : INFINITY;  // a row past the last weighs nothing
-      if (tid == 0) s_bad = 0;
+      if (tid == 0) s_bad[par] = 0;
       fence_proxy_async_smem();
       named_bar_sync(1, 128);
       if (lane == 0) mbar_arrive(&bar_q);
+    };
 
-      // keys visible to every row; those of row r: lim_all + (its query's number)
-      const int lim_all = a.causal ? max(0, q.len - a.nq + 1) : q.len;
-      auto limit = [&](int r) { return a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len; };
-      const uint8_t* kx = C::kCodes ? a.k_exp + (long long)q.slab * a.cap : nullptr;
-      const uint8_t* vx = C::kCodes ? a.v_exp + (long long)q.slab * a.cap : nullptr;
-      int ek = 0, ev = 0;  // exponents of this thread's key, loaded a tile ahead
-      auto load_exps = [&](int i) {
-        const int key = (q.tile0 + i) * kOwnTile + tid;
-        if (C::kCodes && i < q.n && key < q.len) {
-          ek = __ldg(kx + key);
-          ev = __ldg(vx + key);
-        }
-      };
-      load_exps(0);
+    int ek = 0, ev = 0;  // exponents of this thread's key, loaded a tile ahead
+    auto load_exps = [&](const Run& q, int i) {
+      const int key = (q.tile0 + i) * kOwnTile + tid;
+      if (C::kCodes && key < q.len) {
+        const long long at = (long long)q.slab * a.cap + key;
+        ek = __ldg(a.k_exp + at);
+        ev = __ldg(a.v_exp + at);
+      }
+    };
+    // Scores of a chunk of rows as they leave the products (codes: the three terms joined).
+    auto read_chunk = [&](uint32_t at, float (&v)[C::kChunk]) {
+      uint32_t x[C::kTerms][C::kChunk];
+#pragma unroll
+      for (int k = 0; k < C::kTerms; ++k) tmem_ld(at + k * R, x[k]);
+#pragma unroll
+      for (int k = 0; k < C::kTerms; ++k) tmem_ld_wait(x[k]);
+#pragma unroll
+      for (int e = 0; e < C::kChunk; ++e) {
+        v[e] = __uint_as_float(x[0][e]);
+        if constexpr (C::kCodes)
+          v[e] = fmaf(fmaf(__uint_as_float(x[2][e]), 0.0625f, __uint_as_float(x[1][e])), 0.0625f, v[e]);
+      }
+    };
+
+    bool ok = true;
+    unsigned g = 0;
+    int par = 0;
+    Run q, nx;
+    bool have = next_run(walk, q);
+    if (have) {
+      load_q(q);
+      load_exps(q, 0);
+      put_q(q, 0);
+    }
+    while (ok && have) {
+      const int valid = min(R, rows - q.row0);
+      const int lim_all = a.causal ? max(0, q.len - a.nq + 1) : q.len;  // keys that every row sees
+      const RowInfo* row = s_row[par];
       float l[R];  // this thread's share of the normaliser
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.f;
@@ -312,46 +352,43 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         const int key0 = (q.tile0 + i) * kOwnTile, key = key0 + tid;
         const float kf = C::kCodes ? c8::scale(ek) : 1.f;
         const float ve = C::kCodes ? (float)(ev - 127) : 0.f;
-        load_exps(i + 1);
+        if (i + 1 < q.n) {
+          load_exps(q, i + 1);
+        } else {
+          have = next_run(walk, nx);
+          if (have) {
+            load_q(nx);
+            load_exps(nx, 0);
+          }
+        }
         // A wait that gives up leaves its warp in step until the next vote, where all
         // four warps stop together: none may be left alone at a barrier.
-        ok = ok && warp_wait(&bar_s, g & 1, w);
+        ok = ok && warp_wait(&bar_s[g & 1], (g >> 1) & 1, w);
         tc_fence_after();
+        const uint32_t at_s = t_s + (g & 1) * C::kN;
         const bool edge = key0 + kOwnTile > lim_all;
-        float s[R];
+        // ---- do the references hold?
         bool over = false;
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += C::kChunk) {
           if (r0 >= valid) break;
-          uint32_t x[C::kTerms][C::kChunk];
-#pragma unroll
-          for (int k = 0; k < C::kTerms; ++k) tmem_ld(t_s + k * R + r0, x[k]);
-#pragma unroll
-          for (int k = 0; k < C::kTerms; ++k) tmem_ld_wait(x[k]);
+          float v[C::kChunk];
+          read_chunk(at_s + r0, v);
 #pragma unroll
           for (int e = 0; e < C::kChunk; ++e) {
-            const int r = r0 + e;
-            float v = __uint_as_float(x[0][e]);
-            if constexpr (C::kCodes)
-              v = fmaf(fmaf(__uint_as_float(x[2][e]), 0.0625f, __uint_as_float(x[1][e])), 0.0625f, v) * s_rs[r] * kf;
-            else
-              v *= s_rs[r];
-            if (edge && (key >= q.len || key >= limit(r))) v = -INFINITY;
-            s[r] = v;
-            over |= v + ve > s_refw[r] + kRefSlack;
-            if constexpr (C::kCodes) over |= v > s_refl[r] + kSumSlack;
+            float x = v[e] * (row[r0 + e].factor * kf);
+            if (edge && key >= row[r0 + e].limit) x = -INFINITY;
+            over |= x + ve > s_refw[par][r0 + e] + kRefSlack;
+            if constexpr (C::kCodes) over |= x > s_refl[par][r0 + e] + kSumSlack;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_sfree);
-
         // At the edge: values of keys past the end become zero, and so do those that are
         // not finite of keys that only some rows see (0 * NaN would reach the rows that
         // do not); the rows that do see them get them at the run's end.
         if (edge && key >= lim_all) {
-          uint8_t* v = smem + (g % S) * C::kStageBytes;
-          if (!mbar_wait(&bar_fullv[g % S], (g / S) & 1, w))
+          const unsigned h = 2 * g + 1;
+          uint8_t* v = smem + C::kRingOff + (h % H) * C::kTileBytes;
+          if (!mbar_wait(&bar_full[h % H], (h / H) & 1, w))
             ok = false;
           else
             for (int blk = 0; blk < C::kBlocks; ++blk)
@@ -365,26 +402,31 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
                                              finite_only<Kind>(u.w));
                   if (u.x != y.x || u.y != y.y || u.z != y.z || u.w != y.w) {
                     *at = y;
-                    s_bad = 1;
+                    s_bad[par] = 1;
                   }
                 }
               }
         }
         ok = __all_sync(0xffffffffu, ok) != 0;
-        // ---- references.  They stay unless some score outgrew them by more than the slack.
         bool o_done = i == 0;
         if (named_bar_or(1, 128, over || !ok)) {
           if (!named_bar_and(1, 128, ok)) {
             ok = false;
             break;
           }
+#pragma unroll 1
+          for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
+            float v[C::kChunk];
+            read_chunk(at_s + r0, v);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= valid) break;
-            const float mw = warp_max(s[r] + ve), ml = warp_max(s[r]);
-            if (lane == 0) {
-              s_mw[warp][r] = mw;
-              s_ml[warp][r] = ml;
+            for (int e = 0; e < C::kChunk; ++e) {
+              float x = v[e] * (row[r0 + e].factor * kf);
+              if (edge && key >= row[r0 + e].limit) x = -INFINITY;
+              const float mw = warp_max(x + ve), ml = warp_max(x);
+              if (lane == 0) {
+                s_mw[warp][r0 + e] = mw;
+                s_ml[warp][r0 + e] = ml;
+              }
             }
           }
           named_bar_sync(1, 128);
@@ -395,13 +437,17 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
               ref = m;
               return f;
             };
-            s_alw[tid] = grow(s_refw[tid], s_mw[0][tid], s_mw[1][tid], s_mw[2][tid], s_mw[3][tid]);
-            s_all[tid] = grow(s_refl[tid], s_ml[0][tid], s_ml[1][tid], s_ml[2][tid], s_ml[3][tid]);
+            s_fw[tid] = grow(s_refw[par][tid], s_mw[0][tid], s_mw[1][tid], s_mw[2][tid], s_mw[3][tid]);
+            s_fl[tid] = grow(s_refl[par][tid], s_ml[0][tid], s_ml[1][tid], s_ml[2][tid], s_ml[3][tid]);
+            // a row without a key so far (or with -inf scores alone) has reference 0
+            const float rw = s_refw[par][tid], rl = s_refl[par][tid];
+            s_row[par][tid].neg_w = (C::kCodes ? kWeightLog2 : 0.f) - (rw == -INFINITY ? 0.f : rw);
+            s_row[par][tid].neg_l = rl == -INFINITY ? 0.f : -rl;
           }
           named_bar_sync(1, 128);
 #pragma unroll
           for (int r = 0; r < R; ++r)
-            if (r < valid) l[r] *= s_all[r];
+            if (r < valid) l[r] *= s_fl[r];
           if (i > 0) {
             ok = warp_wait(&bar_o, (g - 1) & 1, w);
             o_done = true;
@@ -414,7 +460,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
                 tmem_ld(t_o + k * R + r0, o);
                 tmem_ld_wait(o);
 #pragma unroll
-                for (int e = 0; e < C::kChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_alw[min(r0 + e, R - 1)]);
+                for (int e = 0; e < C::kChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_fw[r0 + e]);
                 tmem_st(t_o + k * R + r0, o);
               }
             tmem_st_wait();
@@ -424,43 +470,55 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         // ---- weights: P^T's place is free once the step before has been added
         if (!o_done) ok = warp_wait(&bar_o, (g - 1) & 1, w);
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          if (r >= valid) break;
-          float x[2];
+        for (int r0 = 0; r0 < R; r0 += C::kChunk) {
+          if (r0 >= valid) break;
+          float v[C::kChunk];
+          read_chunk(at_s + r0, v);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // a row without a key so far (or with -inf scores alone) has reference 0
-            const float rw = s_refw[r + e], nw = rw == -INFINITY ? 0.f : rw;
-            x[e] = ex2_approx(s[r + e] + ve - nw);
+          for (int e = 0; e < C::kChunk; e += 2) {
+            const int r = r0 + e;
+            float x[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const RowInfo info = row[r + y];
+              const float f = info.factor * kf;
+              const bool hidden = edge && key >= info.limit;
+              x[y] = ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_w + ve));
+              if constexpr (C::kCodes)
+                l[r + y] += ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_l));
+              else
+                l[r + y] += x[y];  // the unrounded weights
+            }
             if constexpr (C::kCodes) {
-              const float rl = s_refl[r + e], nl = rl == -INFINITY ? 0.f : rl;
-              l[r + e] += ex2_approx(s[r + e] - nl);
-            } else {
-              l[r + e] += x[e];  // the unrounded weights
-            }
-          }
-          if constexpr (C::kCodes) {
-            uint32_t t[3];
-            c8::encode2_terms(x[0] * kWeightScale, x[1] * kWeightScale, t);
+              uint32_t t[3];
+              c8::encode2_terms(__floats2half2_rn(x[0], x[1]), t);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const int row = k * R + r;
-              sp[swz<128>(row, tid >> 4) + (tid & 15)] = (uint8_t)t[k];
-              sp[swz<128>(row + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[k] >> 8);
+              for (int k = 0; k < 3; ++k) {
+                const int at = k * R + r;
+                sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[k];
+                sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[k] >> 8);
+              }
+            } else {
+              const uint32_t t = pack16x2<Kind == kF16>(x[0], x[1]);
+              uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
+              *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t;
+              *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t >> 16);
             }
-          } else {
-            const uint32_t t = pack16x2<Kind == kF16>(x[0], x[1]);
-            uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
-            *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t;
-            *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t >> 16);
           }
         }
         fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p);
+        if (lane == 0) {
+          mbar_arrive(&bar_sfree[g & 1]);
+          mbar_arrive(&bar_p);
+        }
       }
-      ok = ok && warp_wait(&bar_o, (g - 1) & 1, w);
-      ok = named_bar_and(1, 128, ok);
+      // ---- the next run's queries, while this one's last product runs
+      const unsigned last = g - 1;
+      if (!named_bar_and(1, 128, ok)) break;
+      if (have) put_q(nx, par ^ 1);
+      ok = named_bar_and(1, 128, warp_wait(&bar_o, last & 1, w));
       if (!ok) break;
       tc_fence_after();
 
@@ -474,75 +532,65 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         if (lane == 0) s_ml[warp][r] = x;
       }
       named_bar_sync(1, 128);
+      const long long row_at = (long long)q.slab * rows + q.row0;
       const PartSlot slot = own_slot(a, blockIdx.x, q.tile0 == 0, q.ends, row_at, R, D);
       if (tid < valid)
-        slot.ml[tid] = make_float4(C::kCodes ? s_refl[tid] : s_refw[tid],
-                                   s_ml[0][tid] + s_ml[1][tid] + s_ml[2][tid] + s_ml[3][tid], s_refw[tid], 0.f);
+        slot.ml[tid] = make_float4(s_refl[par][tid], s_ml[0][tid] + s_ml[1][tid] + s_ml[2][tid] + s_ml[3][tid],
+                                   s_refw[par][tid], 0.f);
       if (tid < D) {  // whole warps: lane = element of the head width
 #pragma unroll 1
         for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
-          uint32_t x[C::kTerms][C::kChunk];
-#pragma unroll
-          for (int k = 0; k < C::kTerms; ++k) tmem_ld(t_o + k * R + r0, x[k]);
-#pragma unroll
-          for (int k = 0; k < C::kTerms; ++k) tmem_ld_wait(x[k]);
+          float v[C::kChunk];
+          read_chunk(t_o + r0, v);
 #pragma unroll
           for (int e = 0; e < C::kChunk; ++e) {
             const int r = r0 + e;
-            float v = __uint_as_float(x[0][e]);
-            if constexpr (C::kCodes)
-              v = fmaf(fmaf(__uint_as_float(x[2][e]), 0.0625f, __uint_as_float(x[1][e])), 0.0625f, v) *
-                  (1.f / kWeightScale);
-            if (s_bad != 0 && r < valid) {  // what is not finite of keys that not all rows see
+            if (r >= valid) break;
+            float u = C::kCodes ? v[e] * (1.f / (1 << (int)kWeightLog2)) : v[e];
+            if (s_bad[par] != 0) {  // what is not finite of keys that not all rows see
               const int k0 = max(lim_all, q.tile0 * kOwnTile);
-              const int k1 = min(limit(r), (q.tile0 + q.n) * kOwnTile);
+              const int k1 = min(row[r].limit, (q.tile0 + q.n) * kOwnTile);
               for (int key = k0; key < k1; ++key) {
                 const float y = cache_value<Kind>(static_cast<const uint8_t*>(a.v) +
                                                   (((long long)q.slab * a.cap + key) * D + tid) * C::kElem);
-                if (!(fabsf(y) < INFINITY)) v += y;
+                if (!(fabsf(y) < INFINITY)) u += y;
               }
             }
-            if (r < valid) slot.u[(long long)r * D + tid] = v;
+            slot.u[(long long)r * D + tid] = u;
           }
         }
       }
       tc_fence_before();
-      named_bar_sync(1, 128);  // the next run's shared values follow the last reads of these
+      q = nx;
+      par ^= 1;
     }
   } else if (warp == kOwnTmaWarp && lane == 0) {
     // ------------------------------------------------------------ producer
-    unsigned g = 0;
+    unsigned h = 0;  // tiles of K and V asked for
     bool ok = true;
+    Run q;
     while (ok && next_run(walk, q)) {
-      for (int i = 0; i < q.n; ++i, ++g) {
-        const unsigned s = g % S;
+      for (int i = 0; ok && i < q.n; ++i) {
         const int key0 = (q.tile0 + i) * kOwnTile;
         const int boxes = min(kOwnTile / kBoxKeys, (q.len - key0 + kBoxKeys - 1) / kBoxKeys);
-        uint8_t* v = smem + s * C::kStageBytes;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* free) -> bool {
-          if (g >= S && !mbar_wait(free, (g / S - 1) & 1, w)) return false;
-          mbar_arrive_expect_tx(full, boxes * kBoxKeys * C::kRowBytes);
+        for (int x = 0; x < 2; ++x, ++h) {
+          const unsigned s = h % H;
+          if (h >= H && !mbar_wait(&bar_free[s], (h / H - 1) & 1, w)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bar_full[s], boxes * kBoxKeys * C::kRowBytes);
+          uint8_t* dst = smem + C::kRingOff + s * C::kTileBytes;
           for (int blk = 0; blk < C::kBlocks; ++blk)
-            for (int x = 0; x < boxes; ++x)
-              tma_load_3d(dst + blk * C::kBlockBytes + x * kBoxKeys * C::kPitch, map, full, blk * 64,
-                          key0 + x * kBoxKeys, q.slab);
-          return true;
-        };
-        if (!load(v + C::kTileBytes, &p.tk, &bar_fullk[s], &bar_freek[s]) ||
-            !load(v, &p.tv, &bar_fullv[s], &bar_freev[s])) {
-          ok = false;
-          break;
+            for (int y = 0; y < boxes; ++y)
+              tma_load_3d(dst + blk * C::kBlockBytes + y * kBoxKeys * C::kPitch, x ? &p.tv : &p.tk, &bar_full[s],
+                          blk * 64, key0 + y * kBoxKeys, q.slab);
         }
       }
     }
-    if (abort_flag) {
-      // let copies already in flight land before the CTA's memory is released
-      for (unsigned x = g > S ? g - S : 0; x < g; ++x) {
-        mbar_wait_drain(&bar_fullk[x % S], (x / S) & 1, a.wait_limit_ns);
-        mbar_wait_drain(&bar_fullv[x % S], (x / S) & 1, a.wait_limit_ns);
-      }
-      if (!ok) mbar_wait_drain(&bar_fullk[g % S], (g / S) & 1, a.wait_limit_ns);  // K of the step it gave up in
-    }
+    if (abort_flag)  // let copies already in flight land before the CTA's memory is released
+      for (unsigned x = h > H ? h - H : 0; x < h; ++x)
+        mbar_wait_drain(&bar_full[x % H], (x / H) & 1, a.wait_limit_ns);
   } else if (warp == kOwnMmaWarp && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr int kStep = C::kCodes ? 32 : 16;  // elements of one MMA's reduction
@@ -557,26 +605,27 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       else
         mma_ss(d, x, y, id, acc ? 1u : 0u);
     };
-    const uint64_t dv0 = desc(smem, C::kBlockBytes);  // V^T: MN-major, the next 64 (128) elements a block further
-    const uint64_t dk0 = desc(smem + C::kTileBytes, 16);
+    const uint64_t dk0 = desc(smem + C::kRingOff, 16);
+    const uint64_t dv0 = desc(smem + C::kRingOff, C::kBlockBytes);  // V^T: MN-major, the next elements a block further
     const uint64_t dq0 = desc(smem + C::kQOff, 16);
     const uint64_t dp0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);
     bool ok = true;
     unsigned g = 0;
     int run = 0;
+    Run q;
     // O^T += V^T P^T of step x
     auto add = [&](unsigned x, bool acc) -> bool {
-      const unsigned s = x % S;
-      if (!mbar_wait(&bar_fullv[s], (x / S) & 1, w) || !mbar_wait(&bar_p, x & 1, w)) return false;
+      const unsigned h = 2 * x + 1, s = h % H;
+      if (!mbar_wait(&bar_full[s], (h / H) & 1, w) || !mbar_wait(&bar_p, x & 1, w)) return false;
       tc_fence_after();
-      const uint64_t v = dv0 + ((s * C::kStageBytes) >> 4);
+      const uint64_t v = dv0 + ((s * C::kTileBytes) >> 4);
 #pragma unroll
       for (int k = 0; k < kOwnTile / kStep; ++k) {
         const int byte = k * 32;  // of a row of P^T
-        mma(tmem + C::kN, v + ((k * kStep * C::kPitch) >> 4), dp0 + (((byte >> 7) * C::kPBlock + (byte & 127)) >> 4), id_o,
-            acc || k > 0);
+        mma(tmem + 2 * C::kN, v + ((k * kStep * C::kPitch) >> 4), dp0 + (((byte >> 7) * C::kPBlock + (byte & 127)) >> 4),
+            id_o, acc || k > 0);
       }
-      mma_commit(&bar_freev[s]);
+      mma_commit(&bar_free[s]);
       mma_commit(&bar_o);
       return true;
     };
@@ -584,18 +633,19 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       ok = mbar_wait(&bar_q, run & 1, w);
       ++run;
       for (int i = 0; ok && i < q.n; ++i, ++g) {
-        const unsigned s = g % S;
-        ok = mbar_wait(&bar_fullk[s], (g / S) & 1, w) && (g == 0 || mbar_wait(&bar_sfree, (g - 1) & 1, w));
+        const unsigned h = 2 * g, s = h % H;
+        ok = mbar_wait(&bar_full[s], (h / H) & 1, w) && (g < 2 || mbar_wait(&bar_sfree[g & 1], ((g >> 1) - 1) & 1, w));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t kd = dk0 + ((s * C::kStageBytes) >> 4);
+        const uint64_t kd = dk0 + ((s * C::kTileBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < D / kStep; ++k) {
           const int byte = k * 32, blk = byte / C::kPitch, in = byte % C::kPitch;  // of a row
-          mma(tmem, kd + ((blk * C::kBlockBytes + in) >> 4), dq0 + ((blk * C::kQBlock + in) >> 4), id_s, k > 0);
+          mma(tmem + (g & 1) * C::kN, kd + ((blk * C::kBlockBytes + in) >> 4), dq0 + ((blk * C::kQBlock + in) >> 4), id_s,
+              k > 0);
         }
-        mma_commit(&bar_freek[s]);
-        mma_commit(&bar_s);
+        mma_commit(&bar_free[s]);
+        mma_commit(&bar_s[g & 1]);
         if (i > 0) ok = add(g - 1, i > 1);
       }
       if (ok) ok = add(g - 1, q.n > 1);
@@ -636,12 +686,12 @@ cudaError_t launch_own_k(const ServeArgs& a, int D, bool q_f16, bool after, cuda
     if (r == 4) return launch_own_r<Kind, 64, 4>(a, q_f16, after, s);
     if (r == 8) return launch_own_r<Kind, 64, 8>(a, q_f16, after, s);
     if (r == 16) return launch_own_r<Kind, 64, 16>(a, q_f16, after, s);
-    return launch_own_r<Kind, 64, 32>(a, q_f16, after, s);
+    return launch_own_r<Kind, 64, 24>(a, q_f16, after, s);
   }
   if (r == 4) return launch_own_r<Kind, 128, 4>(a, q_f16, after, s);
   if (r == 8) return launch_own_r<Kind, 128, 8>(a, q_f16, after, s);
   if (r == 16) return launch_own_r<Kind, 128, 16>(a, q_f16, after, s);
-  return launch_own_r<Kind, 128, 32>(a, q_f16, after, s);
+  return launch_own_r<Kind, 128, 24>(a, q_f16, after, s);
 }
 
 }  // namespace
