@@ -61,16 +61,18 @@ __device__ __forceinline__ float2 decode2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Two fp16 values (at most 448 each, or NaN) as sums of three codes each, x = c0 +
-// c1 / 16 + c2 / 256: 4 bits a term, 12 in all (fp16 has 11), down to 2^-18 absolute
-// (half of c2's smallest step, 2^-9 / 256).  Every difference is exact in fp16.
+// Two fp16 values of magnitude at most 256 (or NaN) as sums of three codes each, x =
+// c0 + c1 / 32 + c2 / 1024: 4 bits a term, 12 in all (fp16 has 11), down to 2^-20 absolute (half
+// of c2's smallest step, 2^-9 / 1024).  A term's error is at most 8, so the next one is at most
+// 256 again; every difference is exact in fp16.
+constexpr float kTerm = 1.f / 32;
 __device__ __forceinline__ uint32_t encode2_f16(__half2 h) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
   return r;
 }
 __device__ __forceinline__ void encode2_terms(__half2 h, uint32_t (&t)[3]) {
-  const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
+  const __half2 up = __float2half2_rn(32.f), down = __float2half2_rn(-32.f);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     t[k] = encode2_f16(h);

@@ -12,6 +12,8 @@
 // in front of it drains.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa_internal.cuh"
 #include "fa_serve.cuh"
 #include "ptx.cuh"
@@ -28,6 +30,18 @@ struct MergeParams {
   PrefixPlan pre;
 };
 
+// E (2 or 4) elements, rounded once, in one store.
+template <int E, typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&x)[E]) {
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) w[i] = ptx::pack16x2<std::is_same<T, __half>::value>(x[2 * i], x[2 * i + 1]);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int E = D / 32;
@@ -41,51 +55,96 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
   const int len = raw_len(a, b);
   if (!len_ok(a, len)) return;
   ptx::grid_wait();
+  // ---- where the row's states are: n_pre of the prefix, then n_own of the own rows
+  const long long x = (long long)b * rows + r;  // row of the key head
+  const int unit = hk * p.pre.pairs + (int)(x / (2 * kPrefixRows)), slots = p.pre.split ? 2 : 1;
+  long long pre_at = 0;
+  int n_pre = 0, n_own = 0;
+  if (a.np > 0) {
+    const int c0 = (int)((long long)unit * p.pre.steps / p.pre.per_cta);
+    const int c1 = (int)(((long long)(unit + 1) * p.pre.steps - 1) / p.pre.per_cta);
+    pre_at = ((long long)unit * p.pre.parts * 2 + ((int)(x / kPrefixRows) & 1)) * kPrefixRows + x % kPrefixRows;
+    n_pre = (c1 - c0 + 1) * slots;
+  }
+  const int nt = own_tiles(len), rg = r / p.cta_rows;
+  long long c0 = 0;
+  if (nt > 0) {
+    const long long per = a.plan[0];
+    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * own_cost(nt) + kRunCost;
+    c0 = t0 / per;
+    n_own = (int)((t0 + nt - 1) / per - c0) + 1;
+  }
+  const bool whole = n_own == 1;
+  auto state = [&](int i, const float*& u) -> const float4* {
+    if (i < n_pre) {
+      // part i / slots of the unit; with halved keys both slots hold the row
+      const long long at = pre_at + ((long long)(i / slots) * 2 + i % slots) * kPrefixRows;
+      u = a.pre_u + at * D;
+      return a.pre_ml + at;
+    }
+    if (whole) {
+      u = a.row_u + row * D;
+      return a.row_ml + row;
+    }
+    const int c = i - n_pre;
+    const long long at = ((c0 + c) * 2 + (c == 0 ? 1 : 0)) * p.cta_rows + (r - rg * p.cta_rows);
+    u = a.cut_u + at * D;
+    return a.cut_ml + at;
+  };
+
+  // ---- 32 states at a time: a lane finds one state's share, then all lanes add the rows up
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
   float m = -INFINITY, mu = -INFINITY, l = 0.f, u[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) u[e] = 0.f;
-  auto join = [&](const float* pu, const float4* pml) {
-    const float4 s = *pml;
-    if (s.y == 0.f) return;  // no key (u may not even be written); NaN is not 0
-    const float m_new = fmaxf(m, s.x), mu_new = fmaxf(mu, s.z);
-    l = l * join_factor(m, m_new) + s.y * join_factor(s.x, m_new);
-    const float f = join_factor(mu, mu_new), g = join_factor(s.z, mu_new);
+  const int n = n_pre + n_own;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float* pu = nullptr;
+    float4 s = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (i0 + lane < n) s = *state(i0 + lane, pu);
+    const bool some = s.y != 0.f;  // a state without a key may not even have its u; NaN is not 0
+    const float m_new = fmaxf(m, ptx::warp_max(some ? s.x : -INFINITY));
+    const float mu_new = fmaxf(mu, ptx::warp_max(some ? s.z : -INFINITY));
+    float share = some ? s.y * join_factor(s.x, m_new) : 0.f;
+    const float g = join_factor(s.z, mu_new);
 #pragma unroll
-    for (int e = 0; e < E; ++e) u[e] = u[e] * f + pu[lane * E + e] * g;
+    for (int x = 16; x >= 1; x >>= 1) share += __shfl_xor_sync(0xffffffffu, share, x);
+    l = l * join_factor(m, m_new) + share;
+    const float f = join_factor(mu, mu_new);
+#pragma unroll
+    for (int e = 0; e < E; ++e) u[e] *= f;
     m = m_new;
     mu = mu_new;
-  };
-  if (a.np > 0) {
-    const long long x = (long long)b * rows + r;  // row of the key head
-    const int pair = (int)(x / (2 * kPrefixRows)), slot = (int)(x / kPrefixRows) & 1, in = (int)(x % kPrefixRows);
-    const int unit = hk * p.pre.pairs + pair;
-    const int c0 = (int)((long long)unit * p.pre.steps / p.pre.per_cta);
-    const int c1 = (int)(((long long)(unit + 1) * p.pre.steps - 1) / p.pre.per_cta);
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = ((long long)prefix_part(p.pre, unit, c) * 2 + slot) * kPrefixRows + in;
-      join(a.pre_u + at * D, a.pre_ml + at);
-      if (p.pre.split) join(a.pre_u + (at + kPrefixRows) * D, a.pre_ml + at + kPrefixRows);
-    }
-  }
-  const int nt = own_tiles(len);
-  if (nt > 0) {
-    const int rg = r / p.cta_rows;
-    const long long per = a.plan[0];
-    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * own_cost(nt) + kRunCost;
-    const long long c0 = t0 / per, c1 = (t0 + nt - 1) / per;
-    if (c0 == c1) {
-      join(a.row_u + row * D, a.row_ml + row);
-    } else {
-      for (long long c = c0; c <= c1; ++c) {
-        const long long at = (c * 2 + (c == c0 ? 1 : 0)) * p.cta_rows + (r - rg * p.cta_rows);
-        join(a.cut_u + at * D, a.cut_ml + at);
+    unsigned todo = __ballot_sync(0xffffffffu, some);
+    while (todo) {
+      constexpr int kTogether = 4;  // rows read before the first is used
+      Vec v[kTogether];
+      float w[kTogether];
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        const int i = todo ? __ffs(todo) - 1 : 0;
+        w[k] = __shfl_sync(0xffffffffu, g, i);
+        const float* at = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(pu), i));
+        if (todo)
+          v[k] = reinterpret_cast<const Vec*>(at)[lane];
+        else
+          w[k] = 0.f, v[k] = Vec{};
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        const float* y = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[e] = fmaf(y[e], w[k], u[e]);
       }
     }
   }
   // l = 0: no key; NaN goes through
   const float f = l == 0.f ? 0.f : exp2f(mu - m);
 #pragma unroll
-  for (int e = 0; e < E; ++e) st_elem(static_cast<T*>(a.o), row * D + lane * E + e, l == 0.f ? 0.f : u[e] / l * f);
+  for (int e = 0; e < E; ++e) u[e] = l == 0.f ? 0.f : u[e] / l * f;
+  store_row<E>(static_cast<T*>(a.o) + row * D + lane * E, u);
   if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 

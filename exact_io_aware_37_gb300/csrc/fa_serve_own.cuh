@@ -9,9 +9,9 @@
 // but the narrow side's last columns.
 //
 // The 8-bit cache goes into the products as it is (e4m3, kind::f8f6f4).  A query
-// row is scaled by a power of two and held as three e4m3 terms, x = c0 + c1 / 16 +
-// c2 / 256 (12 bits, as many as fp16 has and more than bf16), each a column of the narrow operand; so
-// are the weights.  A key's power of two multiplies its scores, a value's power of
+// row is scaled by a power of two and held as three e4m3 terms, x = c0 + c1 / 32 +
+// c2 / 1024 (12 bits, more than fp16 or bf16 have), each a column of the narrow operand; so
+// are the weights, rounded to fp16 first.  A key's power of two multiplies its scores, a value's power of
 // two, 2^e, its weight: the weight that is rounded is 2^(s + e - ref_w), with a reference for
 // s + e of its own, so that the largest contribution, not the largest weight, sits
 // at the top of the terms' range however unlike the rows' scales are.  The
@@ -50,17 +50,24 @@ using namespace ptx;
 constexpr int kOwnThreads = 192;
 constexpr int kOwnTmaWarp = 4, kOwnMmaWarp = 5;
 constexpr int kBoxKeys = 32;  // keys of one TMA box: a last tile reads no more boxes than it has keys for
-// Weights are rounded relative to 2^-7 (codes): at most 2 by the reference's rule, so
-// at most 256 of e4m3's 448, and the terms reach down to 2^-18 / 2^7 = 2^-25, as fp16 does.
-constexpr float kWeightLog2 = 7.f;
-constexpr float kRefSlack = 1.f;    // log2 units a weight may outgrow its reference by
-constexpr float kSumSlack = 60.f;   // the same for the float32 normaliser
+// Weights enter the terms times 2^4 and may outgrow their reference by 2^4, so that
+// they stay within 256 and the terms reach down to 2^-20 / 2^4 = 2^-24 of the reference (fp16:
+// 2^-25).  A slack of 2^1 at a scale of 2^7 found new references in every other tile
+// at 20 rows a key head (172 us against 90, 24 ragged sequences up to 16384 keys).
+constexpr float kWeightLog2 = 4.f;
+constexpr float kRefSlack = 4.f;   // log2 units a weight may outgrow its reference by
+constexpr float kSumSlack = 60.f;  // the same for the float32 normaliser
 
 struct OwnParams {
   CUtensorMap tk, tv;
   ServeArgs a;
   int row_groups;
   bool q_f16;  // 8-bit cache: the queries' type (16-bit caches have the queries' type)
+};
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
 };
 
 enum CacheKind { kE4m3, kBf16, kF16 };
@@ -129,9 +136,14 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
 
 // What the threads share about a query row of a run.
 struct RowInfo {
-  float factor;      // from products to log2 units
+  float factor;        // from products to log2 units
   float neg_w, neg_l;  // minus the references (0 without a key so far; neg_w holds the weights' scale)
-  int limit;         // keys it sees
+  int limit;           // keys it sees
+};
+struct RowTest {
+  float factor;
+  float most_w, most_l;  // what the references allow
+  int limit;
 };
 
 template <int Kind, int D, int R>
@@ -148,6 +160,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   __shared__ __align__(8) uint64_t bar_s[2], bar_sfree[2], bar_p, bar_o, bar_q, bar_done;
   // by the run's parity: the next run's are written while this one's are in use
   __shared__ __align__(16) RowInfo s_row[2][R];
+  __shared__ __align__(16) RowTest s_test[2][R];
   __shared__ float s_refw[2][R], s_refl[2][R];  // references of the weights and of the normaliser
   __shared__ float s_mw[4][R], s_ml[4][R];      // warps' maxima, and sums at a run's end
   __shared__ float s_fw[R], s_fl[R];            // rescaling
@@ -271,11 +284,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           }
 #pragma unroll
           for (int m = kRowThreads / 2; m >= 1; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
-          // scaled by a power of two to at most 448: exact in fp16 but for elements below
-          // 2^-14 / 448 of the row's largest (infinities become NaN)
+          // scaled by a power of two to at most 224: exact in fp16 but for elements below
+          // 2^-14 / 224 of the row's largest (infinities become NaN)
           const int eb = c8::exp_byte(big);
-          const float scale = c8::inv_scale(eb);
-          factor *= c8::scale(eb);
+          const float scale = 0.5f * c8::inv_scale(eb);
+          factor *= 2.f * c8::scale(eb);
           uint32_t t[4][3];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -295,8 +308,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         if (r < R && qx == 0) {
           // a row past the last weighs nothing and outgrows nothing
           const bool there = r < valid;
-          s_row[par][r] = RowInfo{factor, there ? 0.f : -INFINITY, there ? 0.f : -INFINITY,
-                                  a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len};
+          const int limit = a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len;
+          s_row[par][r] = RowInfo{factor, there ? 0.f : -INFINITY, there ? 0.f : -INFINITY, limit};
+          s_test[par][r] = RowTest{factor, there ? -INFINITY : INFINITY, there ? -INFINITY : INFINITY, limit};
           s_refw[par][r] = s_refl[par][r] = there ? -INFINITY : INFINITY;
         }
       }
@@ -326,7 +340,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       for (int e = 0; e < C::kChunk; ++e) {
         v[e] = __uint_as_float(x[0][e]);
         if constexpr (C::kCodes)
-          v[e] = fmaf(fmaf(__uint_as_float(x[2][e]), 0.0625f, __uint_as_float(x[1][e])), 0.0625f, v[e]);
+          v[e] = fmaf(fmaf(__uint_as_float(x[2][e]), c8::kTerm, __uint_as_float(x[1][e])), c8::kTerm, v[e]);
       }
     };
 
@@ -369,19 +383,25 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         const bool edge = key0 + kOwnTile > lim_all;
         // ---- do the references hold?
         bool over = false;
+        auto look = [&](auto at_edge) {
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += C::kChunk) {
-          if (r0 >= valid) break;
-          float v[C::kChunk];
-          read_chunk(at_s + r0, v);
+          for (int r0 = 0; r0 < R; r0 += C::kChunk) {
+            if (r0 >= valid) break;
+            float v[C::kChunk];
+            read_chunk(at_s + r0, v);
 #pragma unroll
-          for (int e = 0; e < C::kChunk; ++e) {
-            float x = v[e] * (row[r0 + e].factor * kf);
-            if (edge && key >= row[r0 + e].limit) x = -INFINITY;
-            over |= x + ve > s_refw[par][r0 + e] + kRefSlack;
-            if constexpr (C::kCodes) over |= x > s_refl[par][r0 + e] + kSumSlack;
+            for (int e = 0; e < C::kChunk; ++e) {
+              const RowTest t = s_test[par][r0 + e];
+              const float x = v[e] * (t.factor * kf);
+              const bool more = x > (C::kCodes ? fminf(t.most_w - ve, t.most_l) : t.most_w);
+              over |= at_edge.value ? more && key < t.limit : more;
+            }
           }
-        }
+        };
+        if (edge)
+          look(Flag<true>{});
+        else
+          look(Flag<false>{});
         // At the edge: values of keys past the end become zero, and so do those that are
         // not finite of keys that only some rows see (0 * NaN would reach the rows that
         // do not); the rows that do see them get them at the run's end.
@@ -443,6 +463,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             const float rw = s_refw[par][tid], rl = s_refl[par][tid];
             s_row[par][tid].neg_w = (C::kCodes ? kWeightLog2 : 0.f) - (rw == -INFINITY ? 0.f : rw);
             s_row[par][tid].neg_l = rl == -INFINITY ? 0.f : -rl;
+            s_test[par][tid].most_w = rw + kRefSlack;
+            s_test[par][tid].most_l = rl + kSumSlack;
           }
           named_bar_sync(1, 128);
 #pragma unroll
@@ -469,43 +491,50 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         }
         // ---- weights: P^T's place is free once the step before has been added
         if (!o_done) ok = warp_wait(&bar_o, (g - 1) & 1, w);
+        auto weigh = [&](auto at_edge) {
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += C::kChunk) {
-          if (r0 >= valid) break;
-          float v[C::kChunk];
-          read_chunk(at_s + r0, v);
+          for (int r0 = 0; r0 < R; r0 += C::kChunk) {
+            if (r0 >= valid) break;
+            float v[C::kChunk];
+            read_chunk(at_s + r0, v);
 #pragma unroll
-          for (int e = 0; e < C::kChunk; e += 2) {
-            const int r = r0 + e;
-            float x[2];
+            for (int e = 0; e < C::kChunk; e += 2) {
+              const int r = r0 + e;
+              if (r >= valid) break;
+              float x[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const RowInfo info = row[r + y];
-              const float f = info.factor * kf;
-              const bool hidden = edge && key >= info.limit;
-              x[y] = ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_w + ve));
-              if constexpr (C::kCodes)
-                l[r + y] += ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_l));
-              else
-                l[r + y] += x[y];  // the unrounded weights
-            }
-            if constexpr (C::kCodes) {
-              uint32_t t[3];
-              c8::encode2_terms(__floats2half2_rn(x[0], x[1]), t);
-#pragma unroll
-              for (int k = 0; k < 3; ++k) {
-                const int at = k * R + r;
-                sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[k];
-                sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[k] >> 8);
+              for (int y = 0; y < 2; ++y) {
+                const RowInfo info = row[r + y];
+                const float f = info.factor * kf;
+                const bool hidden = at_edge.value && key >= info.limit;
+                x[y] = ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_w + ve));
+                if constexpr (C::kCodes)
+                  l[r + y] += ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_l));
+                else
+                  l[r + y] += x[y];  // the unrounded weights
               }
-            } else {
-              const uint32_t t = pack16x2<Kind == kF16>(x[0], x[1]);
-              uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
-              *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t;
-              *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t >> 16);
+              if constexpr (C::kCodes) {
+                uint32_t t[3];
+                c8::encode2_terms(__floats2half2_rn(x[0], x[1]), t);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                  const int at = k * R + r;
+                  sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[k];
+                  sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[k] >> 8);
+                }
+              } else {
+                const uint32_t t = pack16x2<Kind == kF16>(x[0], x[1]);
+                uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
+                *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t;
+                *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t >> 16);
+              }
             }
           }
-        }
+        };
+        if (edge)
+          weigh(Flag<true>{});
+        else
+          weigh(Flag<false>{});
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();

@@ -57,13 +57,15 @@ def o_bound(O, A, S, n, D, vmax, out_dtype, p_dtype):
     A score is a float32 sum of D products (each at most one step of 2^-23 of
     the running sum, which S bounds) and enters 2^x with a step of 2^-23 of its
     own size and 2^-22 of the exponential's: e = (D + 4) 2^-23 S + 2^-22 relative to each weight.
-    The weights are rounded to p_dtype (half a step u_p, and 2^-25 absolute
-    where fp16 becomes subnormal, for weights relative to their largest), summed with n float32 additions in
+    The weights are rounded to p_dtype (half a step u_p, and for fp16 2^-24
+    absolute, for weights relative to their largest: fp16's subnormals end at
+    2^-25, the 8-bit cache's weights in three e4m3 terms, c0 + c1 / 32 + c2 / 1024 times
+    2^-4, at half of 2^-9 / 1024 / 16 = 2^-24), summed with n float32 additions in
     the numerator and in the denominator, and the quotient is rounded to
     out_dtype (half a step u_o)."""
     u_o, u_p = torch.finfo(out_dtype).eps / 2, torch.finfo(p_dtype).eps / 2
     e = (D + 4) * 2.0 ** -23 * S + 2.0 ** -22
-    tiny = 2.0 ** -25 * n * vmax if p_dtype == torch.float16 else 0.0
+    tiny = 2.0 ** -24 * n * vmax if p_dtype == torch.float16 else 0.0
     rel = u_p + 2 * e + 2 * n * 2.0 ** -23
     return u_o * np.abs(O) + (rel[..., None] * A + tiny) * (1 + u_o) + torch.finfo(out_dtype).smallest_normal * u_o
 
