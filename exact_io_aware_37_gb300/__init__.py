@@ -310,73 +310,80 @@ def cache_alloc(B, Hk, cap, D, device="cuda"):
     return Cache8(k, v, k_exp, v_exp)
 
 
-def _check_cuda(*tensors):
-    """_check, and that the tensors (the first one sets the device) are on a GPU."""
-    if not tensors[0].is_cuda:
+# A decoding step of a small batch takes the GPU a few microseconds, so these
+# calls keep their own host cost down: one pass over the tensors, the stream's
+# handle straight from torch (torch.cuda.current_stream builds an object, 3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _elsewhere(t, stream):
+    """Whether a call on t has to make another device or stream current first;
+    refuses tensors that are not on a GPU."""
+    if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    _check(*tensors)
+    return stream is not None or t.get_device() != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
-def _other(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-        with torch.cuda.stream(stream):
-            yield
-
-
-_HERE = contextlib.nullcontext()
-
-
 def _on(t, stream):
     """Makes t's device and `stream` (None: that device's current one) current
     for a call, so that its scratch and outputs are allocated for the stream
     that writes them."""
-    if stream is None and t.get_device() == torch.cuda.current_device():
-        return _HERE
-    return _other(t.device, stream)
+    with torch.cuda.device(t.device):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+        with torch.cuda.stream(stream):
+            yield
 
 
-def _check_cache8(cache):
-    k, v, k_exp, v_exp = cache
-    if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k.shape[:3]:
+def _together(device, tensors):
+    for t in tensors:
+        if t is not None and (t.get_device() != device or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on one device")
+
+
+def _check_cache8(k, v, k_exp, v_exp):
+    if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k_exp.shape:
         raise ValueError("a cache holds k, v [B, Hk, cap, D] and k_exp, v_exp [B, Hk, cap]")
-    if k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype:
+    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
         raise ValueError("cache codes must be float8_e4m3fn")
     if k_exp.dtype != torch.uint8 or v_exp.dtype != torch.uint8:
         raise ValueError("cache exponents must be uint8")
 
 
 def _check_int32(name, t, B):
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B:
         raise ValueError(f"{name} must be int32 [{B}]")
 
 
-def _raise(st, where):
-    if st != 0:
-        raise FAError(st, where)
-
-
-def _rows_call(fn, where, k, v, cache, start, count, stream):
-    cache = Cache8(*cache)
-    _check_cuda(k, v, *cache, start, count)
-    _check_cache8(cache)
-    B, H, cap, D = cache.k.shape
+def _rows_call(where, k, v, cache, start, count, stream):
+    kc, vc, ke, ve = cache
+    if _elsewhere(k, stream):
+        with _on(k, stream):
+            return _rows_call(where, k, v, cache, start, count, None)
+    device = k.get_device()
+    _together(device, (k, v, kc, vc, ke, ve, start, count))
+    _check_cache8(kc, vc, ke, ve)
+    B, H, cap, D = kc.shape
     if k.dim() != 4 or v.shape != k.shape or (k.shape[0], k.shape[1], k.shape[3]) != (B, H, D):
         raise ValueError("k and v must be [B, Hk, n, D] with the cache's B, Hk and D")
-    if v.dtype != k.dtype or k.dtype not in _DT:
+    dt = _DT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
         raise ValueError("k and v must be both bfloat16, float16 or float32")
-    _check_int32("start", start, B)
-    _check_int32("count", count, B)
-    n = k.shape[2]
-    dense, held = (_ptr(k), _ptr(v)), tuple(map(_ptr, cache))
-    with _on(k, stream):
-        _raise(fn(*(dense + held if where == "fa_cache_write" else held + dense), B, H, n, cap, D, _ptr(start),
-                  _ptr(count), _DT[k.dtype], _stream(stream)), where)
+    at_start = at_count = None
+    if start is not None:
+        _check_int32("start", start, B)
+        at_start = start.data_ptr()
+    if count is not None:
+        _check_int32("count", count, B)
+        at_count = count.data_ptr()
+    dense = (k.data_ptr(), v.data_ptr())
+    held = (kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr())
+    st = getattr(lib(), where)(*(dense + held if where == "fa_cache_write" else held + dense), B, H, k.shape[2], cap, D,
+                               at_start, at_count, dt, _raw_stream(device))
+    if st != 0:
+        raise FAError(st, where)
 
 
 def fa_cache_write(k, v, cache, start=None, count=None, stream=None):
@@ -385,75 +392,105 @@ def fa_cache_write(k, v, cache, start=None, count=None, stream=None):
     count: int32 [B] on the device; None: 0 and n).  Rows that are not
     addressed keep what they hold; a sequence whose range does not fit in the
     cache is skipped and reported by fa_get_last_device_error."""
-    _rows_call(lib().fa_cache_write, "fa_cache_write", k, v, cache, start, count, stream)
+    _rows_call("fa_cache_write", k, v, cache, start, count, stream)
 
 
 def fa_cache_read(cache, k, v, start=None, count=None, stream=None):
     """Read rows start[b] .. start[b] + count[b] - 1 of the 8-bit cache into k,
     v [B, Hk, n, D] (bf16, fp16 or fp32); the rows after them become zeros."""
-    _rows_call(lib().fa_cache_read, "fa_cache_read", k, v, cache, start, count, stream)
+    _rows_call("fa_cache_read", k, v, cache, start, count, stream)
 
 
 def cache_read(cache, start, n, count=None, dtype=torch.bfloat16, stream=None):
     """Allocating wrapper around fa_cache_read: returns (k, v) [B, Hk, n, D]."""
-    B, H, _, D = cache[0].shape
-    with _on(cache[0], stream):
-        k, v = (torch.empty(B, H, n, D, dtype=dtype, device=cache[0].device) for _ in range(2))
-    fa_cache_read(cache, k, v, start, count, stream)
+    held = cache[0]
+    if _elsewhere(held, stream):
+        with _on(held, stream):
+            return cache_read(cache, start, n, count, dtype)
+    B, H, _, D = held.shape
+    k, v = torch.empty(2, B, H, n, D, dtype=dtype, device=held.device).unbind(0)
+    _rows_call("fa_cache_read", k, v, cache, start, count, None)
     return k, v
 
 
-def _serve_dims(q, cache, max_len):
+def _serve_dims(q, held, max_len):
     """(B, H, Hk, nq, cap, max_len, D) of a decoding step over a cache."""
-    if q.dim() != 4 or cache[0].dim() != 4:
+    if q.dim() != 4 or held.dim() != 4:
         raise ValueError("q must be [B, H, nq, D] and the cache [B, Hk, cap, D]")
     B, H, nq, D = q.shape
-    Bk, Hk, cap, Dk = cache[0].shape
+    Bk, Hk, cap, Dk = held.shape
     if Bk != B or Dk != D or Hk == 0 or H % Hk:
         raise ValueError("q [B, H, nq, D] needs a cache [B, Hk, cap, D] with H a multiple of Hk")
-    max_len = cap if max_len is None else int(max_len)
+    if max_len is None:
+        return B, H, Hk, nq, cap, cap, D
+    max_len = int(max_len)
     if not 0 <= max_len <= cap:
         raise ValueError("max_len must be between 0 and the cache's capacity")
     return B, H, Hk, nq, cap, max_len, D
 
 
 def _serve_call(where, q, prefix, cache, lens, o, lse, causal, scale, max_len, workspace, stream):
-    B, H, Hk, nq, cap, max_len, D = _serve_dims(q, cache, max_len)
+    """The decoding steps over a cache; allocates what is None, returns (o, lse)."""
+    B, H, Hk, nq, cap, max_len, D = _serve_dims(q, cache[0], max_len)
+    dtype = q.dtype
     if len(cache) == 4:
-        _check_cache8(cache)
-    elif len(cache) != 2 or cache[1].shape != cache[0].shape or cache[0].dtype != q.dtype or cache[1].dtype != q.dtype:
+        _check_cache8(*cache)
+        held = tuple([t.data_ptr() for t in cache])
+    elif len(cache) == 2 and cache[1].shape == cache[0].shape and cache[0].dtype == cache[1].dtype == dtype:
+        held = (cache[0].data_ptr(), cache[1].data_ptr(), None, None)
+    else:
         raise ValueError("the cache must be a Cache8, or a pair k, v [B, Hk, cap, D] of q's dtype")
-    _check_cuda(q, *prefix, *cache, lens, o, lse, workspace)
-    if q.dtype not in _DT or o.dtype != q.dtype or o.shape != q.shape:
-        raise ValueError("o must have q's shape and dtype")
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
-        raise ValueError("lse must be float32 [B, H, nq]")
-    _check_int32("lens", lens, B)
-    np_ = 0
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return _serve_call(where, q, prefix, cache, lens, o, lse, causal, scale, max_len, workspace, None)
+    device = q.get_device()
+    dt = _DT.get(dtype)
+    if dt is None:
+        raise ValueError("q must be bfloat16 or float16")
+    if o is None:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, nq), dtype=torch.float32, device=q.device)
+    else:
+        if o.dtype != dtype or o.shape != q.shape:
+            raise ValueError("o must have q's shape and dtype")
+        if lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
+            raise ValueError("lse must be float32 [B, H, nq]")
+        _together(device, (o, lse, workspace))
+    _together(device, (q, lens, *cache, *prefix))
+    at_lens = None
+    if lens is not None:
+        _check_int32("lens", lens, B)
+        at_lens = lens.data_ptr()
+    n_prefix = 0
     if prefix:
         kp, vp = prefix
         if kp.dim() != 3 or vp.shape != kp.shape or kp.shape[0] != Hk or kp.shape[2] != D:
             raise ValueError("the prefix must be k, v [Hk, np, D]")
-        if kp.dtype != q.dtype or vp.dtype != q.dtype:
+        if kp.dtype != dtype or vp.dtype != dtype:
             raise ValueError("the prefix must have q's dtype")
-        np_ = kp.shape[1]
-    dt = _DT[q.dtype]
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with _on(q, stream):
-        if workspace is None:
-            need = lib().fa_decode_shared_workspace_size(B, H, Hk, nq, np_, max_len, D, dt)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        head = (_ptr(q),) + (tuple(map(_ptr, prefix)) if prefix else ())
-        held = tuple(map(_ptr, cache)) if len(cache) == 4 else (_ptr(cache[0]), _ptr(cache[1]), None, None)
-        sizes = (B, H, Hk, nq, np_, cap, max_len, D) if prefix else (B, H, Hk, nq, cap, max_len, D)
-        _raise(getattr(lib(), where)(*head, *held, _ptr(o), _ptr(lse), *sizes, scale, int(bool(causal)), _ptr(lens), dt,
-                                     _ptr(workspace), nbytes, _stream(stream)), where)
+        n_prefix = kp.shape[1]
+        head = (q.data_ptr(), kp.data_ptr(), vp.data_ptr())
+        sizes = (B, H, Hk, nq, n_prefix, cap, max_len, D)
+    else:
+        head = (q.data_ptr(),)
+        sizes = (B, H, Hk, nq, cap, max_len, D)
+    library = lib()
+    if workspace is None:
+        nbytes = library.fa_decode_shared_workspace_size(B, H, Hk, nq, n_prefix, max_len, D, dt)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    st = getattr(library, where)(*head, *held, o.data_ptr(), lse.data_ptr(), *sizes,
+                                 1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, at_lens, dt,
+                                 workspace.data_ptr(), nbytes, _raw_stream(device))
+    if st != 0:
+        raise FAError(st, where)
+    return o, lse
 
 
 def fa_decode_cache_workspace_size(q, cache, max_len=None):
     """Bytes of scratch fa_decode_cache needs for q [B, H, nq, D] and this cache."""
-    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache, max_len)
+    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache[0], max_len)
     return int(lib().fa_decode_cache_workspace_size(B, H, Hk, nq, max_len, D, _DT[q.dtype]))
 
 
@@ -465,23 +502,22 @@ def fa_decode_cache(q, cache, lens, o, lse, causal, scale=None, max_len=None, wo
     Query i is at position lens[b] - nq + i.  max_len (default: the capacity)
     bounds lens.  Writes o (dtype of q) and lse [B, H, nq] (float32); rows that
     see no key get 0 and -inf."""
-    cache = Cache8(*cache)
+    if len(cache) != 4:
+        raise ValueError("the cache must be a Cache8")
     _serve_call("fa_decode_cache", q, (), cache, lens, o, lse, causal, scale, max_len, workspace, stream)
 
 
 def decode_cache(q, cache, lens=None, causal=True, scale=None, max_len=None, stream=None):
     """Allocating wrapper around fa_decode_cache: returns (o, lse)."""
-    with _on(q, stream):
-        o = torch.empty_like(q)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fa_decode_cache(q, cache, lens, o, lse, causal, scale, max_len, stream=stream)
-    return o, lse
+    if len(cache) != 4:
+        raise ValueError("the cache must be a Cache8")
+    return _serve_call("fa_decode_cache", q, (), cache, lens, None, None, causal, scale, max_len, None, stream)
 
 
 def fa_decode_shared_workspace_size(q, k_prefix, cache, max_len=None):
     """Bytes of scratch fa_decode_shared needs for q [B, H, nq, D], a prefix
     k_prefix [Hk, np, D] and the sequences' own cache."""
-    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache, max_len)
+    B, H, Hk, nq, _, max_len, D = _serve_dims(q, cache[0], max_len)
     return int(lib().fa_decode_shared_workspace_size(B, H, Hk, nq, k_prefix.shape[1], max_len, D, _DT[q.dtype]))
 
 
@@ -492,14 +528,11 @@ def fa_decode_shared(q, k_prefix, v_prefix, cache, lens, o, lse, causal, scale=N
     each sequence's own, in `cache`: a Cache8, or a pair k, v [B, Hk, cap, D] of
     q's dtype.  Query i is at position np + lens[b] - nq + i.  Everything else
     as for fa_decode_cache."""
-    _serve_call("fa_decode_shared", q, (k_prefix, v_prefix), tuple(cache), lens, o, lse, causal, scale, max_len,
+    _serve_call("fa_decode_shared", q, (k_prefix, v_prefix), cache, lens, o, lse, causal, scale, max_len,
                 workspace, stream)
 
 
 def decode_shared(q, k_prefix, v_prefix, cache, lens=None, causal=True, scale=None, max_len=None, stream=None):
     """Allocating wrapper around fa_decode_shared: returns (o, lse)."""
-    with _on(q, stream):
-        o = torch.empty_like(q)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fa_decode_shared(q, k_prefix, v_prefix, cache, lens, o, lse, causal, scale, max_len, stream=stream)
-    return o, lse
+    return _serve_call("fa_decode_shared", q, (k_prefix, v_prefix), cache, lens, None, None, causal, scale, max_len,
+                       None, stream)
