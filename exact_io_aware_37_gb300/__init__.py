@@ -408,7 +408,7 @@ def cache_read(cache, start, n, count=None, dtype=torch.bfloat16, stream=None):
         with _on(held, stream):
             return cache_read(cache, start, n, count, dtype)
     B, H, _, D = held.shape
-    k, v = torch.empty(2, B, H, n, D, dtype=dtype, device=held.device).unbind(0)
+    k, v = (torch.empty((B, H, n, D), dtype=dtype, device=held.device) for _ in range(2))
     _rows_call("fa_cache_read", k, v, cache, start, count, None)
     return k, v
 

@@ -52,94 +52,97 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
   if (row >= (long long)a.B * a.Hk * rows) return;
   const long long slab = row / rows;
   const int r = (int)(row - slab * rows), b = (int)(slab / a.Hk), hk = (int)(slab - (long long)b * a.Hk);
-  const int len = raw_len(a, b);
-  if (!len_ok(a, len)) return;
-  ptx::grid_wait();
-  // ---- where the row's states are: n_pre of the prefix, then n_own of the own rows
-  const long long x = (long long)b * rows + r;  // row of the key head
-  const int unit = hk * p.pre.pairs + (int)(x / (2 * kPrefixRows)), slots = p.pre.split ? 2 : 1;
-  long long pre_at = 0;
-  int n_pre = 0, n_own = 0;
+  // ---- where the prefix's states are (nothing here hangs on the kernels in front)
+  const int slots = p.pre.split ? 2 : 1;
+  int n_pre = 0;
+  const float* pre_u = nullptr;
+  const float4* pre_ml = nullptr;
   if (a.np > 0) {
+    const long long x = (long long)b * rows + r;  // row of the key head
+    const int unit = hk * p.pre.pairs + (int)(x / (2 * kPrefixRows));
     const int c0 = (int)((long long)unit * p.pre.steps / p.pre.per_cta);
     const int c1 = (int)(((long long)(unit + 1) * p.pre.steps - 1) / p.pre.per_cta);
-    pre_at = ((long long)unit * p.pre.parts * 2 + ((int)(x / kPrefixRows) & 1)) * kPrefixRows + x % kPrefixRows;
+    const long long tile = (long long)unit * p.pre.parts * 2 + ((int)(x / kPrefixRows) & 1);
     n_pre = (c1 - c0 + 1) * slots;
+    // lane i reads state i's share; its own columns (groups of eight) of any state
+    pre_ml = a.pre_ml + tile * kPrefixRows + x % kPrefixRows;
+    pre_u = a.pre_u + tile * kPrefixRows * D + x % kPrefixRows * 8 + lane * E / 8 * (kPrefixRows * 8) + lane * E % 8;
   }
+  const int len = raw_len(a, b);
+  if (!len_ok(a, len)) return;
   const int nt = own_tiles(len), rg = r / p.cta_rows;
-  long long c0 = 0;
+  ptx::grid_wait();
+  long long per = 0, base = 0;
   if (nt > 0) {
-    const long long per = a.plan[0];
-    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * own_cost(nt) + kRunCost;
-    c0 = t0 / per;
-    n_own = (int)((t0 + nt - 1) / per - c0) + 1;
+    per = a.plan[0];
+    base = a.plan[1 + b];
   }
-  const bool whole = n_own == 1;
-  auto state = [&](int i, const float*& u) -> const float4* {
-    if (i < n_pre) {
-      // part i / slots of the unit; with halved keys both slots hold the row
-      const long long at = pre_at + ((long long)(i / slots) * 2 + i % slots) * kPrefixRows;
-      u = a.pre_u + at * D;
-      return a.pre_ml + at;
-    }
-    if (whole) {
-      u = a.row_u + row * D;
-      return a.row_ml + row;
-    }
-    const int c = i - n_pre;
-    const long long at = ((c0 + c) * 2 + (c == 0 ? 1 : 0)) * p.cta_rows + (r - rg * p.cta_rows);
-    u = a.cut_u + at * D;
-    return a.cut_ml + at;
-  };
 
-  // ---- 32 states at a time: a lane finds one state's share, then all lanes add the rows up
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   float m = -INFINITY, mu = -INFINITY, l = 0.f, u[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) u[e] = 0.f;
-  const int n = n_pre + n_own;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const float* pu = nullptr;
-    float4 s = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    if (i0 + lane < n) s = *state(i0 + lane, pu);
-    const bool some = s.y != 0.f;  // a state without a key may not even have its u; NaN is not 0
-    const float m_new = fmaxf(m, ptx::warp_max(some ? s.x : -INFINITY));
-    const float mu_new = fmaxf(mu, ptx::warp_max(some ? s.z : -INFINITY));
-    float share = some ? s.y * join_factor(s.x, m_new) : 0.f;
-    const float g = join_factor(s.z, mu_new);
+  // Adds n states: 32 at a time, a lane finds one state's share (s: its own of the first 32), then all
+  // lanes add the rows up.  at(i): where state i is, in steps from ml and pu.
+  const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  auto join = [&](int n, float4 s, const float4* ml, const float* pu, long long ml_step, long long u_step, auto at) {
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      if (i0 > 0) s = i0 + lane < n ? ml[at(i0 + lane) * ml_step] : none;
+      const bool some = s.y != 0.f;  // a state without a key may not even have its u; NaN is not 0
+      const float m_new = fmaxf(m, ptx::warp_max(some ? s.x : -INFINITY));
+      const float mu_new = fmaxf(mu, ptx::warp_max(some ? s.z : -INFINITY));
+      float share = some ? s.y * join_factor(s.x, m_new) : 0.f;
+      const float g = join_factor(s.z, mu_new);
+      unsigned todo = __ballot_sync(0xffffffffu, some);
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) share += __shfl_xor_sync(0xffffffffu, share, x);
-    l = l * join_factor(m, m_new) + share;
-    const float f = join_factor(mu, mu_new);
+      for (int x = 16; x >= 1; x >>= 1) share += __shfl_xor_sync(0xffffffffu, share, x);
+      l = l * join_factor(m, m_new) + share;
+      const float f = join_factor(mu, mu_new);
 #pragma unroll
-    for (int e = 0; e < E; ++e) u[e] *= f;
-    m = m_new;
-    mu = mu_new;
-    unsigned todo = __ballot_sync(0xffffffffu, some);
-    while (todo) {
-      constexpr int kTogether = 4;  // rows read before the first is used
-      Vec v[kTogether];
-      float w[kTogether];
+      for (int e = 0; e < E; ++e) u[e] *= f;
+      m = m_new;
+      mu = mu_new;
+      while (todo) {
+        constexpr int kTogether = 8;  // rows read before the first is used
+        Vec v[kTogether];
+        float w[kTogether];
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) {
-        const int i = todo ? __ffs(todo) - 1 : 0;
-        w[k] = __shfl_sync(0xffffffffu, g, i);
-        const float* at = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(pu), i));
-        if (todo)
-          v[k] = reinterpret_cast<const Vec*>(at)[lane];
-        else
-          w[k] = 0.f, v[k] = Vec{};
-        todo &= todo - 1;
-      }
+        for (int k = 0; k < kTogether; ++k) {
+          const int i = todo ? __ffs(todo) - 1 : 0;
+          w[k] = todo ? __shfl_sync(0xffffffffu, g, i) : 0.f;
+          v[k] = todo ? *reinterpret_cast<const Vec*>(pu + at(i0 + i) * u_step) : Vec{};
+          todo &= todo - 1;
+        }
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) {
-        const float* y = reinterpret_cast<const float*>(&v[k]);
+        for (int k = 0; k < kTogether; ++k) {
+          const float* y = reinterpret_cast<const float*>(&v[k]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = fmaf(y[e], w[k], u[e]);
+          for (int e = 0; e < E; ++e) u[e] = fmaf(y[e], w[k], u[e]);
+        }
       }
     }
+  };
+  // part i / slots of the unit; with halved keys both slots hold the row
+  const auto pre_at = [&](int i) -> long long { return (long long)(i / slots) * 2 + i % slots; };
+  const float4 pre_s = lane < n_pre ? pre_ml[pre_at(lane) * kPrefixRows] : none;
+  // the own rows' first shares are on their way while the prefix's states are added
+  int n_own = 0;
+  const float4* own_ml = a.row_ml + row;
+  const float* own_u = a.row_u + row * D + lane * E;
+  if (nt > 0) {
+    const long long t0 = base + ((long long)hk * p.row_groups + rg) * own_cost(a, nt) + a.run_cost;
+    const long long c0 = t0 / per;
+    n_own = (int)((t0 + nt - 1) / per - c0) + 1;
+    if (n_own > 1) {
+      const long long first = c0 * 2 * p.cta_rows + (r - rg * p.cta_rows);
+      own_ml = a.cut_ml + first;
+      own_u = a.cut_u + first * D + lane * E;
+    }
   }
+  const auto own_at = [&](int i) -> long long { return n_own == 1 ? 0 : i == 0 ? 1 : 2 * (long long)i; };
+  const float4 own_s = lane < n_own ? own_ml[own_at(lane) * p.cta_rows] : none;
+  join(n_pre, pre_s, pre_ml, pre_u, kPrefixRows, (long long)kPrefixRows * D, pre_at);
+  join(n_own, own_s, own_ml, own_u, p.cta_rows, (long long)p.cta_rows * D, own_at);
   // l = 0: no key; NaN goes through
   const float f = l == 0.f ? 0.f : exp2f(mu - m);
 #pragma unroll
@@ -198,6 +201,7 @@ size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, 
 
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s) {
   const bool f16 = dt == FA_F16;
+  a.run_cost = own_run_cost(a.k_exp ? 1 : 2, D);
   MergeParams m;
   m.cta_rows = own_rows(a.group * a.nq);
   m.row_groups = (a.group * a.nq + m.cta_rows - 1) / m.cta_rows;

@@ -212,11 +212,12 @@ struct ServeArgs {
   unsigned long long wait_limit_ns;
   // workspace: states of the own rows' units (fa_serve.cuh)
   long long* plan;  // [1 + B]
+  int run_cost;     // of a run of the own rows, in tiles
   float* row_u;     // [B * H * nq, D] units that one CTA covers
   float4* row_ml;
   float* cut_u;  // [2 * CTAs, rows of a CTA, D] the ends of the others
   float4* cut_ml;
-  float* pre_u;  // [parts of all units, 2 slots, rows of a slot, D] the prefix's states
+  float* pre_u;  // [parts of all units, 2 slots, D / 8, rows of a slot, 8] the prefix's states
   float4* pre_ml;
 };
 struct PrefixPlan;

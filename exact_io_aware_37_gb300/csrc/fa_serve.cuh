@@ -17,9 +17,10 @@ namespace fa {
 constexpr int kOwnCtas = 304;
 constexpr int kOwnTile = 128;  // keys of a step
 // What a run costs besides its tiles (queries in, references found, state out), in tiles: it
-// only steers the cut.  Measured on 32 ragged sequences of 4 to 2048 keys, 32 key heads: without it the CTAs
-// that got the short sequences took twice the average.
-constexpr int kRunCost = 2;
+// only steers the cut.  About as long as 96 KB of cache take: fitted over the CTAs of
+// ragged batches, 3 tiles of 32 KB (8-bit, D = 128, up to 16 rows; 5 at 24 rows), below
+// one of 64 KB (16-bit).  Without it the CTAs that got the short sequences took twice the average.
+inline int own_run_cost(int elem_bytes, int D) { return (96 * 1024) / (2 * kOwnTile * D * elem_bytes); }
 // Query rows of a CTA: what the rows of a key head fill, so that fewer rows leave fewer
 // columns to multiply and read out.  More than 24 are spread over row groups, which
 // read the same keys at about the same time, so mostly from L2.
@@ -37,14 +38,14 @@ __device__ __forceinline__ int seq_len(const ServeArgs& a, int b) {
 }
 __device__ __forceinline__ int own_tiles(int len) { return (int)(((unsigned)len + kOwnTile - 1) / kOwnTile); }
 // Cost of a unit of `tiles` tiles: the run's own cost, then a tile each.
-__device__ __forceinline__ int own_cost(int tiles) { return tiles > 0 ? tiles + kRunCost : 0; }
+__device__ __forceinline__ int own_cost(const ServeArgs& a, int tiles) { return tiles > 0 ? tiles + a.run_cost : 0; }
 
 // Factor of a state with maximum m joined under the maximum mm >= m: 1 for
 // equal maxima, -inf among them (that state holds nothing, or only NaN).
 __device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }
 
 // A CTA's share [first, end) of the cost of all sequences laid out in a row
-// (sequence-major, units of a sequence, in a unit kRunCost and then its tiles); `base`
+// (sequence-major, units of a sequence, in a unit the run's own cost and then its tiles); `base`
 // lies before sequence b, which holds position `first`.  A tile belongs to the CTA whose
 // share its position falls into.
 struct OwnPlan {
@@ -67,7 +68,7 @@ __device__ __forceinline__ void own_plan(const ServeArgs& a, int units, OwnPlan&
       if (blockIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
       return 0;
     }
-    return (long long)own_cost(own_tiles(len)) * units;
+    return (long long)own_cost(a, own_tiles(len)) * units;
   };
   const long long mine = cost(threadIdx.x);  // the first kThreads sequences: enough for most batches
   long long x = mine;

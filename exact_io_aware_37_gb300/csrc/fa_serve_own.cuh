@@ -134,6 +134,25 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
+// Sums of R values a lane over the warp: l[0] of lane x becomes the sum of value x % R2,
+// R2 the power of two from R on (values past R count as 0).  R2 - 1 + log2(32 / R2) shuffles, not 5 R.
+template <int R>
+__device__ __forceinline__ void sum_rows(float (&l)[R], int lane) {
+  constexpr int R2 = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
+#pragma unroll
+  for (int half = R2 / 2; half >= 1; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int r = 0; r < half; ++r) {
+      const float a = r < R ? l[r] : 0.f, b = r + half < R ? l[r + half] : 0.f;
+      const float got = __shfl_xor_sync(0xffffffffu, up ? a : b, half);
+      if (r < R) l[r] = (up ? b : a) + got;
+    }
+  }
+#pragma unroll
+  for (int m = R2; m < 32; m <<= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], m);
+}
+
 // What the threads share about a query row of a run.
 struct RowInfo {
   float factor;        // from products to log2 units
@@ -215,7 +234,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   auto next_run = [&](Walk& k, Run& q) -> bool {
     while (k.t < plan.end) {
       q.len = seq_len(a, k.b);
-      const int nt = own_tiles(q.len), cost = own_cost(nt);
+      const int nt = own_tiles(q.len), cost = own_cost(a, nt);
       const long long here = (long long)cost * units;
       if (k.t >= k.base + here) {
         k.base += here;
@@ -227,8 +246,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       const int x0 = (int)(at - (long long)unit * cost);
       const int x1 = (int)min((long long)cost, x0 + (plan.end - k.t));
       k.t += x1 - x0;
-      q.tile0 = max(0, x0 - kRunCost);
-      q.n = max(0, x1 - kRunCost) - q.tile0;
+      q.tile0 = max(0, x0 - a.run_cost);
+      q.n = max(0, x1 - a.run_cost) - q.tile0;
       if (q.n <= 0) continue;  // the share ends before the unit's first tile
       q.ends = x1 == cost;
       q.b = k.b;
@@ -442,7 +461,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             for (int e = 0; e < C::kChunk; ++e) {
               float x = v[e] * (row[r0 + e].factor * kf);
               if (edge && key >= row[r0 + e].limit) x = -INFINITY;
-              const float mw = warp_max(x + ve), ml = warp_max(x);
+              const float mw = warp_max(x + ve), ml = C::kCodes ? warp_max(x) : mw;
               if (lane == 0) {
                 s_mw[warp][r0 + e] = mw;
                 s_ml[warp][r0 + e] = ml;
@@ -552,23 +571,13 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       tc_fence_after();
 
       // ---- the run's state
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r >= valid) break;
-        float x = l[r];
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-        if (lane == 0) s_ml[warp][r] = x;
-      }
-      named_bar_sync(1, 128);
       const long long row_at = (long long)q.slab * rows + q.row0;
       const PartSlot slot = own_slot(a, blockIdx.x, q.tile0 == 0, q.ends, row_at, R, D);
-      if (tid < valid)
-        slot.ml[tid] = make_float4(s_refl[par][tid], s_ml[0][tid] + s_ml[1][tid] + s_ml[2][tid] + s_ml[3][tid],
-                                   s_refw[par][tid], 0.f);
       if (tid < D) {  // whole warps: lane = element of the head width
-#pragma unroll 1
-        for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
+        const bool bad = s_bad[par] != 0;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += C::kChunk) {
+          if (r0 >= valid) break;
           float v[C::kChunk];
           read_chunk(t_o + r0, v);
 #pragma unroll
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             const int r = r0 + e;
             if (r >= valid) break;
             float u = C::kCodes ? v[e] * (1.f / (1 << (int)kWeightLog2)) : v[e];
-            if (s_bad[par] != 0) {  // what is not finite of keys that not all rows see
+            if (bad) {  // what is not finite of keys that not all rows see
               const int k0 = max(lim_all, q.tile0 * kOwnTile);
               const int k1 = min(row[r].limit, (q.tile0 + q.n) * kOwnTile);
               for (int key = k0; key < k1; ++key) {
@@ -589,6 +598,16 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           }
         }
       }
+      // The rows' sums over the keys: at every step a lane passes half of its rows on and keeps
+      // the other half's sums, so that in the end lane x has row x of the first kRows2 rows
+      // (lanes that share a row hold equal sums).
+      sum_rows<R>(l, lane);
+      constexpr int kRows2 = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
+      if (lane < R && lane < kRows2) s_ml[warp][lane] = l[0];
+      named_bar_sync(1, 128);
+      if (tid < valid)
+        slot.ml[tid] = make_float4(s_refl[par][tid], s_ml[0][tid] + s_ml[1][tid] + s_ml[2][tid] + s_ml[3][tid],
+                                   s_refw[par][tid], 0.f);
       tc_fence_before();
       q = nx;
       par ^= 1;
@@ -641,7 +660,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     bool ok = true;
     unsigned g = 0;
     int run = 0;
-    Run q;
+    Run q, nx;
     // O^T += V^T P^T of step x
     auto add = [&](unsigned x, bool acc) -> bool {
       const unsigned h = 2 * x + 1, s = h % H;
@@ -658,7 +677,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       mma_commit(&bar_o);
       return true;
     };
-    while (ok && next_run(walk, q)) {
+    bool have = next_run(walk, q);
+    while (ok && have) {
       ok = mbar_wait(&bar_q, run & 1, w);
       ++run;
       for (int i = 0; ok && i < q.n; ++i, ++g) {
@@ -677,7 +697,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         mma_commit(&bar_s[g & 1]);
         if (i > 0) ok = add(g - 1, i > 1);
       }
+      have = next_run(walk, nx);  // while the softmax works
       if (ok) ok = add(g - 1, q.n > 1);
+      q = nx;
     }
     // every MMA issued must be complete before tensor memory is released
     mma_commit(&bar_done);

@@ -24,7 +24,7 @@
 //
 // Warps and barriers are those of the forward, except that the softmax warps
 // write their own Q tile into shared memory (rows of one tile come from many
-// sequences) and announce it, with the slot's columns free, on bar_q[t].
+// sequences) and announce it on bar_q[t], a run's before they read out the last one's state.
 #include <math.h>
 
 #include "fa_internal.cuh"
@@ -138,39 +138,60 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t t_s = tmem + lane_off + t * 128;
     const uint32_t t_o = tmem + lane_off + 256 + t * 128;
+    // A run's query row to this slot's tile; kmax: the prefix keys that the row sees.
+    // Every S of the slot's run before is complete.
+    auto put_q = [&](const Run& q, int& kmax) {
+      const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;  // row of the key head
+      const int b = row / gq, rr = row - b * gq;
+      const uint4* src = nullptr;
+      kmax = 0;
+      if (row < rows) {
+        const int len = raw_len(a, b);
+        if (len_ok(a, len)) {
+          kmax = a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
+          src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                               (((long long)b * a.Hk + q.hk) * gq + rr) * D);
+        }
+      }
+      // kLanes lanes read a row together (a row a lane would touch 32 lines an access: 4 us)
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+#pragma unroll
+      for (int i0 = 0; i0 < kLanes; i0 += 8) {  // eight loads in flight; more would spill
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const auto* from = reinterpret_cast<const uint4*>(__shfl_sync(
+              0xffffffffu, reinterpret_cast<unsigned long long>(src), (i0 + i) * kAtOnce + lane / kLanes));
+          x[i] = from ? __ldg(from + lane % kLanes) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int to = quad * 32 + (i0 + i) * kAtOnce + lane / kLanes, ch = lane % kLanes;  // tile row, 16-byte chunk
+          *reinterpret_cast<uint4*>(smem + C::kQOff + t * C::kTileBytes + (ch >> 3) * C::kHalfBytes + to * 128 +
+                                    (((ch & 7) ^ (to & 7)) << 4)) = x[i];
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_q[t]);
+    };
     bool ok = true;
     int G = 0;   // steps of the earlier runs
     int cs = 0;  // completions of bar_s[t] seen so far
     long long cur = first;
-    Run q;
-    while (ok && next_run(cur, q)) {
+    Run q, nx;
+    int kmax = 0, kmax_next = 0;
+    bool have = next_run(cur, q), ready = false;
+    while (ok && have) {
+      have = next_run(cur, nx);
       if (t < q.slots) {
-        const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;  // row of the key head
-        const int b = row / gq, rr = row - b * gq;
-        int kmax = 0;  // prefix keys that the row sees
-        {
-          uint8_t* dst = smem + C::kQOff + t * C::kTileBytes + r * 128;
-          const uint4* src = nullptr;
-          if (row < rows) {
-            const int len = raw_len(a, b);
-            if (len_ok(a, len)) {
-              kmax = a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
-              src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                   (((long long)b * a.Hk + q.hk) * gq + rr) * D);
-            }
-          }
-          // the slot's previous S products are complete (its last P V was waited for below)
-#pragma unroll
-          for (int hf = 0; hf < C::kHalves; ++hf)
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4*>(dst + hf * C::kHalfBytes + ((ch ^ (r & 7)) << 4)) =
-                  src ? __ldg(src + hf * 8 + ch) : make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_q[t]);
-        }
+        const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;
+        if (ready)
+          kmax = kmax_next;
+        else
+          put_q(q, kmax);
+        ready = false;
         const bool work = __any_sync(0xffffffffu, kmax > 0);  // a warp without a row only keeps step
         float m_ref = -INFINITY;  // reference maximum of the exponentials (log2 units)
         float l = 0.f;
@@ -260,27 +281,27 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_p[t]);
         }
+        // the next run's queries, while this one's last product runs: its S is issued
+        // after that product, over the weights that it has read by then
+        if (ok && have && t < nx.slots) {
+          put_q(nx, kmax_next);
+          ready = true;
+        }
         if (ok && warp_wait(&bar_s[t], cs & 1, w)) {
           ++cs;
           tc_fence_after();
-          // the run's state: rows leave as whole 128-byte segments (an 8 x 8 exchange of
-          // 16-byte chunks inside groups of eight lanes)
+          // the run's state, in groups of eight columns: a warp's rows are neighbours there
           const long long at = ((long long)q.part * 2 + t) * kBM;
           if (work) {
-            const int grp = lane & ~7, sub = lane & 7;
+            float* u = a.pre_u + at * D + r * 8;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld32(t_o + c, o);
               tmem_ld_wait(o);
-              exchange_chunks<8>(o, lane);
+              if (row < rows)
 #pragma unroll
-              for (int s8 = 0; s8 < 8; ++s8) {
-                const int x = quad * 32 + grp + s8;
-                if (q.row0 + (kSplit ? 0 : t * kBM) + x < rows)
-                  *reinterpret_cast<uint4*>(a.pre_u + (at + x) * D + c + sub * 4) =
-                      make_uint4(o[4 * s8], o[4 * s8 + 1], o[4 * s8 + 2], o[4 * s8 + 3]);
-              }
+                for (int x = 0; x < 32; x += 8) store32(u + ((c + x) >> 3) * (kBM * 8), o + x);
             }
           }
           if (row < rows) a.pre_ml[at + r] = make_float4(m_ref, l, work ? m_ref : -INFINITY, 0.f);
@@ -289,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
         }
       }
       G += q.n;
+      q = nx;
     }
   } else {
     // warps 8-11: producer, MMA issuer and two idle warps completing the warpgroup
