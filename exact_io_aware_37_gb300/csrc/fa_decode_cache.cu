@@ -5,8 +5,8 @@
 // queries sits at position total - nq + i of its sequence's total = np + len
 // keys, so causal allows key j iff j <= i + total - nq.
 //
-// A step is up to three launches: the pass over the prefix (fa_tc_prefix.cu), the
-// pass over the own rows (fa_serve_own.cuh), and the join of the states they
+// A step is up to three launches: the pass over the own rows (fa_serve_own.cuh), the
+// pass over the prefix (fa_tc_prefix.cu), and the join of the states they
 // leave, here: m = max m_s, l = sum l_s 2^(m_s - m), u = sum u_s 2^(mu_s - mu),
 // O = u 2^(mu - m) / l, L = (m + log2 l) ln 2.  Each launch may start while the one
 // in front of it drains.
@@ -208,9 +208,9 @@ cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cuda
   m.pre = prefix_plan(a.B, a.Hk, a.group * a.nq, a.np);
   carve(a, D, m.pre, static_cast<char*>(workspace));
   cudaError_t e = cudaSuccess;
-  if (a.np > 0) e = launch_prefix(a, m.pre, D, f16, s);
-  if (e == cudaSuccess && a.max_len > 0)
-    e = a.k_exp ? launch_own_e4m3(a, D, f16, a.np > 0, s) : launch_own_16(a, D, f16, a.np > 0, s);
+  // The own rows first: where their shares end unevenly the prefix's CTAs, all alike, move in.
+  if (a.max_len > 0) e = a.k_exp ? launch_own_e4m3(a, D, f16, s) : launch_own_16(a, D, f16, s);
+  if (e == cudaSuccess && a.np > 0) e = launch_prefix(a, m.pre, D, f16, a.max_len > 0, s);
   if (e != cudaSuccess) return e;
   m.a = a;
   return f16 ? launch_merge<__half>(m, D, s) : launch_merge<__nv_bfloat16>(m, D, s);

@@ -93,7 +93,8 @@ struct OwnCfg {
   // at D = 64 the second half of V^T's 128 rows is read from what follows V (its products go to
   // tensor-memory lanes that nothing reads); past the ring's last slot that is this many bytes
   static constexpr int kPad = D == 64 ? kTileBytes : 0;
-  // as many slots as leave room for a second CTA on the SM, if that is three
+  // as many slots as leave room for a second CTA on the SM, if that is three (a third CTA, at the
+  // same bytes in flight, gained nothing)
   static constexpr int kFit = (110 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kSlots = kFit >= 3 ? (kFit < 8 ? kFit : 8) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
@@ -173,10 +174,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // Steps (tiles) g are counted over all of a CTA's runs.  full / free: the ring; bar_s[g % 2]:
-  // S^T(g) complete; bar_sfree[g % 2]: read out; bar_p: P^T(g) written; bar_o: O^T += (g)
-  // complete; bar_q: a run's Q written.
+  // S^T(g) complete; bar_p: P^T(g) written and S^T(g) read out (the MMA thread has waited for
+  // it before it issues S^T(g + 2) over the same columns); bar_o: O^T += (g) complete; bar_q: a
+  // run's Q written.
   __shared__ __align__(8) uint64_t bar_full[H], bar_free[H];
-  __shared__ __align__(8) uint64_t bar_s[2], bar_sfree[2], bar_p, bar_o, bar_q, bar_done;
+  __shared__ __align__(8) uint64_t bar_s[2], bar_p, bar_o, bar_q, bar_done;
   // by the run's parity: the next run's are written while this one's are in use
   __shared__ __align__(16) RowInfo s_row[2][R];
   __shared__ __align__(16) RowTest s_test[2][R];
@@ -198,10 +200,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_free[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar_s[s], 1);
-      mbar_init(&bar_sfree[s], 4);
-    }
+    for (int s = 0; s < 2; ++s) mbar_init(&bar_s[s], 1);
     mbar_init(&bar_p, 4);
     mbar_init(&bar_o, 1);
     mbar_init(&bar_q, 4);
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 
   // ---- the CTA's runs, walked alike by every role
   struct Run {
-    int b, len, row0, slab, tile0, n;
+    int len, row0, slab, tile0, n;
     bool ends;  // the run holds the unit's last tile
   };
   struct Walk {
@@ -250,7 +249,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       q.n = max(0, x1 - a.run_cost) - q.tile0;
       if (q.n <= 0) continue;  // the share ends before the unit's first tile
       q.ends = x1 == cost;
-      q.b = k.b;
       const int hk = unit / p.row_groups;
       q.row0 = (unit - hk * p.row_groups) * R;
       q.slab = k.b * a.Hk + hk;
@@ -557,10 +555,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar_sfree[g & 1]);
-          mbar_arrive(&bar_p);
-        }
+        if (lane == 0) mbar_arrive(&bar_p);
       }
       // ---- the next run's queries, while this one's last product runs
       const unsigned last = g - 1;
@@ -683,7 +678,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       ++run;
       for (int i = 0; ok && i < q.n; ++i, ++g) {
         const unsigned h = 2 * g, s = h % H;
-        ok = mbar_wait(&bar_full[s], (h / H) & 1, w) && (g < 2 || mbar_wait(&bar_sfree[g & 1], ((g >> 1) - 1) & 1, w));
+        ok = mbar_wait(&bar_full[s], (h / H) & 1, w);
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = dk0 + ((s * C::kTileBytes) >> 4);
@@ -709,12 +704,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   tc_fence_before();
   __syncthreads();
   if (warp == kOwnMmaWarp) tmem_dealloc(tmem, C::kCols);
-  // this kernel's end has to mean the end of the pass over the prefix too
-  if (threadIdx.x == 0) grid_wait();
 }
 
 template <int Kind, int D, int R>
-cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, bool after, cudaStream_t s) {
+cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, cudaStream_t s) {
   using C = OwnCfg<Kind, D, R>;
   OwnParams p;
   p.a = a;
@@ -727,22 +720,22 @@ cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, bool after, cudaStream_
   const cudaError_t e = cudaFuncSetAttribute(own_kernel<Kind, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return note_error("cached decoding smem attribute", e);
   return note_error("cached decoding launch", launch_serve_kernel(own_kernel<Kind, D, R>, kOwnCtas / 2 * C::kPerSm,
-                                                                  kOwnThreads, C::kSmem, after, s, p));
+                                                                  kOwnThreads, C::kSmem, false, s, p));
 }
 
 template <int Kind>
-cudaError_t launch_own_k(const ServeArgs& a, int D, bool q_f16, bool after, cudaStream_t s) {
+cudaError_t launch_own_k(const ServeArgs& a, int D, bool q_f16, cudaStream_t s) {
   const int r = own_rows(a.group * a.nq);
   if (D == 64) {
-    if (r == 4) return launch_own_r<Kind, 64, 4>(a, q_f16, after, s);
-    if (r == 8) return launch_own_r<Kind, 64, 8>(a, q_f16, after, s);
-    if (r == 16) return launch_own_r<Kind, 64, 16>(a, q_f16, after, s);
-    return launch_own_r<Kind, 64, 24>(a, q_f16, after, s);
+    if (r == 4) return launch_own_r<Kind, 64, 4>(a, q_f16, s);
+    if (r == 8) return launch_own_r<Kind, 64, 8>(a, q_f16, s);
+    if (r == 16) return launch_own_r<Kind, 64, 16>(a, q_f16, s);
+    return launch_own_r<Kind, 64, 24>(a, q_f16, s);
   }
-  if (r == 4) return launch_own_r<Kind, 128, 4>(a, q_f16, after, s);
-  if (r == 8) return launch_own_r<Kind, 128, 8>(a, q_f16, after, s);
-  if (r == 16) return launch_own_r<Kind, 128, 16>(a, q_f16, after, s);
-  return launch_own_r<Kind, 128, 24>(a, q_f16, after, s);
+  if (r == 4) return launch_own_r<Kind, 128, 4>(a, q_f16, s);
+  if (r == 8) return launch_own_r<Kind, 128, 8>(a, q_f16, s);
+  if (r == 16) return launch_own_r<Kind, 128, 16>(a, q_f16, s);
+  return launch_own_r<Kind, 128, 24>(a, q_f16, s);
 }
 
 }  // namespace

@@ -69,10 +69,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // bar_k0: the first K tile; bar_kv[g % stages]: V_g and K_{g+1}.  Steps g are counted
-  // over all of the CTA's runs, so rings and per-step barriers keep their phase.
+  // over all of the CTA's runs, so rings and per-step barriers keep their phase.  bar_s[t]: an S of
+  // slot t (and the P V before it); bar_fin[t]: a run's last P V.  That one has a barrier of its own because
+  // the next run's first S may be complete before the softmax looks: two phases of one barrier
+  // would pass for none.
   __shared__ __align__(8) uint64_t bar_k0, bar_done;
   __shared__ __align__(8) uint64_t bar_kv[C::kStages], bar_kfree[C::kStages], bar_vfree[C::kStages];
-  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2];
+  __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_fin[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
 
@@ -113,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
       mbar_init(&bar_q[t], 4);  // one arrival per softmax warp
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_fin[t], 1);
     }
     abort_flag = 0;
     fence_mbar_init();
@@ -145,13 +149,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
       const int b = row / gq, rr = row - b * gq;
       const uint4* src = nullptr;
       kmax = 0;
+      int len = -1;
       if (row < rows) {
-        const int len = raw_len(a, b);
-        if (len_ok(a, len)) {
-          kmax = a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
-          src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                               (((long long)b * a.Hk + q.hk) * gq + rr) * D);
-        }
+        len = raw_len(a, b);  // on its way while the queries are read
+        src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                             (((long long)b * a.Hk + q.hk) * gq + rr) * D);
       }
       // kLanes lanes read a row together (a row a lane would touch 32 lines an access: 4 us)
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
@@ -171,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
                                     (((ch & 7) ^ (to & 7)) << 4)) = x[i];
         }
       }
+      if (len_ok(a, len))
+        kmax = a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     };
     bool ok = true;
     int G = 0;   // steps of the earlier runs
-    int cs = 0;  // completions of bar_s[t] seen so far
+    int cs = 0, fin = 0;  // completions of bar_s[t] and bar_fin[t] seen so far
     long long cur = first;
     Run q, nx;
     int kmax = 0, kmax_next = 0;
@@ -287,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
           put_q(nx, kmax_next);
           ready = true;
         }
-        if (ok && warp_wait(&bar_s[t], cs & 1, w)) {
-          ++cs;
+        if (ok && warp_wait(&bar_fin[t], fin & 1, w)) {
+          ++fin;
           tc_fence_after();
           // the run's state, in groups of eight columns: a warp's rows are neighbours there
           const long long at = ((long long)q.part * 2 + t) * kBM;
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
             tc_fence_after();
             issue_pv(t, s, j > 0);
             if (j + 1 < q.n) issue_s(t, s1);
-            mma_commit(&bar_s[t]);
+            mma_commit(j + 1 < q.n ? &bar_s[t] : &bar_fin[t]);
           }
         }
         G += q.n;
@@ -467,10 +471,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  // this kernel's end has to mean the end of the pass over the own rows too
+  if (threadIdx.x == 0) grid_wait();
 }
 
 template <int D, bool F16, bool kSplit>
-cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
+cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, bool after, cudaStream_t s) {
   using C = Cfg<D>;
   PrefixParams p;
   p.a = a;
@@ -481,19 +487,19 @@ cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, cudaStre
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return note_error("prefix smem attribute", e);
   return note_error("prefix launch", launch_serve_kernel(tc_prefix_kernel<D, F16, kSplit>, plan.ctas, kThreads,
-                                                         C::kSmemBytes, false, s, p));
+                                                         C::kSmemBytes, after, s, p));
 }
 
 template <int D, bool F16>
-cudaError_t launch_prefix_f(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
-  return plan.split ? launch_prefix_d<D, F16, true>(a, plan, s) : launch_prefix_d<D, F16, false>(a, plan, s);
+cudaError_t launch_prefix_f(const ServeArgs& a, const PrefixPlan& plan, bool after, cudaStream_t s) {
+  return plan.split ? launch_prefix_d<D, F16, true>(a, plan, after, s) : launch_prefix_d<D, F16, false>(a, plan, after, s);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, cudaStream_t s) {
-  if (D == 64) return f16 ? launch_prefix_f<64, true>(a, plan, s) : launch_prefix_f<64, false>(a, plan, s);
-  return f16 ? launch_prefix_f<128, true>(a, plan, s) : launch_prefix_f<128, false>(a, plan, s);
+cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, bool after, cudaStream_t s) {
+  if (D == 64) return f16 ? launch_prefix_f<64, true>(a, plan, after, s) : launch_prefix_f<64, false>(a, plan, after, s);
+  return f16 ? launch_prefix_f<128, true>(a, plan, after, s) : launch_prefix_f<128, false>(a, plan, after, s);
 }
 
 }  // namespace fa
