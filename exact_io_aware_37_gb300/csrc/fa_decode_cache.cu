@@ -21,8 +21,13 @@
 namespace fa {
 namespace {
 
-// Joins the states of every query row: a warp a row.
-constexpr int kMergeWarps = 8;
+// Joins the states of every query row: D / 8 lanes a row, eight columns each, one
+// whole sector of a state's row.  The join waits for L2 more than it moves bytes, so
+// where few rows have many states kGroups groups of lanes share a row's (2048 rows of 17 states:
+// four groups 51 us a step, one 66; 3840 rows of 2: 112 and 107; 8192 rows of 7: 139 and 135).
+constexpr int kMergeThreads = 256;
+constexpr long long kFewRows = 4096;
+constexpr int kManyStates = 6;
 
 struct MergeParams {
   ServeArgs a;
@@ -30,28 +35,18 @@ struct MergeParams {
   PrefixPlan pre;
 };
 
-// E (2 or 4) elements, rounded once, in one store.
-template <int E, typename T>
-__device__ __forceinline__ void store_row(T* p, const float (&x)[E]) {
-  uint32_t w[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) w[i] = ptx::pack16x2<std::is_same<T, __half>::value>(x[2 * i], x[2 * i + 1]);
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(p) = w[0];
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_constant__ MergeParams p) {
-  constexpr int E = D / 32;
+template <typename T, int D, int kGroups>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int kLanes = D / 8, kTogether = 4;  // lanes of a row; states' rows read before the first is used
   const ServeArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % kLanes;
   const int rows = a.group * a.nq;
-  const long long row = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.Hk * rows) return;
-  const long long slab = row / rows;
-  const int r = (int)(row - slab * rows), b = (int)(slab / a.Hk), hk = (int)(slab - (long long)b * a.Hk);
+  constexpr int kBlockRows = kMergeThreads / kLanes / kGroups;
+  const int group = threadIdx.x / kLanes % kGroups, in_block = threadIdx.x / kLanes / kGroups;
+  const long long row = (long long)blockIdx.x * kBlockRows + in_block;
+  const bool there = row < (long long)a.B * a.Hk * rows;  // every lane stays for the shuffles
+  const long long slab = there ? row / rows : 0;
+  const int r = there ? (int)(row - slab * rows) : 0, b = (int)(slab / a.Hk), hk = (int)(slab - (long long)b * a.Hk);
   // ---- where the prefix's states are (nothing here hangs on the kernels in front)
   const int slots = p.pre.split ? 2 : 1;
   int n_pre = 0;
@@ -64,99 +59,151 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
     const int c1 = (int)(((long long)(unit + 1) * p.pre.steps - 1) / p.pre.per_cta);
     const long long tile = (long long)unit * p.pre.parts * 2 + ((int)(x / kPrefixRows) & 1);
     n_pre = (c1 - c0 + 1) * slots;
-    // lane i reads state i's share; its own columns (groups of eight) of any state
     pre_ml = a.pre_ml + tile * kPrefixRows + x % kPrefixRows;
-    pre_u = a.pre_u + tile * kPrefixRows * D + x % kPrefixRows * 8 + lane * E / 8 * (kPrefixRows * 8) + lane * E % 8;
+    pre_u = a.pre_u + tile * kPrefixRows * D + x % kPrefixRows * 8 + lane * (kPrefixRows * 8);
   }
   const int len = raw_len(a, b);
-  if (!len_ok(a, len)) return;
-  const int nt = own_tiles(len), rg = r / p.cta_rows;
+  const bool valid = there && len_ok(a, len);
+  const int nt = valid ? own_tiles(len) : 0, rg = r / p.cta_rows;
+  if (!valid) n_pre = 0;
   ptx::grid_wait();
-  long long per = 0, base = 0;
-  if (nt > 0) {
-    per = a.plan[0];
-    base = a.plan[1 + b];
-  }
-
-  using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  float m = -INFINITY, mu = -INFINITY, l = 0.f, u[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) u[e] = 0.f;
-  // Adds n states: 32 at a time, a lane finds one state's share (s: its own of the first 32), then all
-  // lanes add the rows up.  at(i): where state i is, in steps from ml and pu.
-  const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-  auto join = [&](int n, float4 s, const float4* ml, const float* pu, long long ml_step, long long u_step, auto at) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      if (i0 > 0) s = i0 + lane < n ? ml[at(i0 + lane) * ml_step] : none;
-      const bool some = s.y != 0.f;  // a state without a key may not even have its u; NaN is not 0
-      const float m_new = fmaxf(m, ptx::warp_max(some ? s.x : -INFINITY));
-      const float mu_new = fmaxf(mu, ptx::warp_max(some ? s.z : -INFINITY));
-      float share = some ? s.y * join_factor(s.x, m_new) : 0.f;
-      const float g = join_factor(s.z, mu_new);
-      unsigned todo = __ballot_sync(0xffffffffu, some);
-#pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) share += __shfl_xor_sync(0xffffffffu, share, x);
-      l = l * join_factor(m, m_new) + share;
-      const float f = join_factor(mu, mu_new);
-#pragma unroll
-      for (int e = 0; e < E; ++e) u[e] *= f;
-      m = m_new;
-      mu = mu_new;
-      while (todo) {
-        constexpr int kTogether = 8;  // rows read before the first is used
-        Vec v[kTogether];
-        float w[kTogether];
-#pragma unroll
-        for (int k = 0; k < kTogether; ++k) {
-          const int i = todo ? __ffs(todo) - 1 : 0;
-          w[k] = todo ? __shfl_sync(0xffffffffu, g, i) : 0.f;
-          v[k] = todo ? *reinterpret_cast<const Vec*>(pu + at(i0 + i) * u_step) : Vec{};
-          todo &= todo - 1;
-        }
-#pragma unroll
-        for (int k = 0; k < kTogether; ++k) {
-          const float* y = reinterpret_cast<const float*>(&v[k]);
-#pragma unroll
-          for (int e = 0; e < E; ++e) u[e] = fmaf(y[e], w[k], u[e]);
-        }
-      }
-    }
-  };
   // part i / slots of the unit; with halved keys both slots hold the row
-  const auto pre_at = [&](int i) -> long long { return (long long)(i / slots) * 2 + i % slots; };
+  // (this group's are i kGroups + group)
+  const auto mine = [&](int n) { return (n - group + kGroups - 1) / kGroups; };
+  const auto pre_at = [&](int i) -> long long {
+    i = i * kGroups + group;
+    return (long long)(i / slots) * 2 + i % slots;
+  };
+  n_pre = mine(n_pre);
+  const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
   const float4 pre_s = lane < n_pre ? pre_ml[pre_at(lane) * kPrefixRows] : none;
-  // the own rows' first shares are on their way while the prefix's states are added
   int n_own = 0;
   const float4* own_ml = a.row_ml + row;
-  const float* own_u = a.row_u + row * D + lane * E;
+  const float* own_u = a.row_u + row * D + lane * 8;
   if (nt > 0) {
-    const long long t0 = base + ((long long)hk * p.row_groups + rg) * own_cost(a, nt) + a.run_cost;
+    const long long per = a.plan[0];
+    const long long t0 = a.plan[1 + b] + ((long long)hk * p.row_groups + rg) * own_cost(a, nt) + a.run_cost;
     const long long c0 = t0 / per;
     n_own = (int)((t0 + nt - 1) / per - c0) + 1;
     if (n_own > 1) {
       const long long first = c0 * 2 * p.cta_rows + (r - rg * p.cta_rows);
       own_ml = a.cut_ml + first;
-      own_u = a.cut_u + first * D + lane * E;
+      own_u = a.cut_u + first * D + lane * 8;
     }
   }
-  const auto own_at = [&](int i) -> long long { return n_own == 1 ? 0 : i == 0 ? 1 : 2 * (long long)i; };
-  const float4 own_s = lane < n_own ? own_ml[own_at(lane) * p.cta_rows] : none;
+  const bool whole = n_own == 1;
+  const auto own_at = [&](int i) -> long long {
+    i = i * kGroups + group;
+    return whole ? 0 : i == 0 ? 1 : 2 * (long long)i;
+  };
+  n_own = mine(n_own);
+  const float4 own_s = lane < n_own ? own_ml[own_at(lane) * p.cta_rows] : none;  // on its way while the prefix's are added
+
+  float m = -INFINITY, mu = -INFINITY, l = 0.f, u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = 0.f;
+  // Adds n states, kLanes at a time: a lane finds one state's share (s: its own of the first kLanes), then
+  // all lanes add the rows up.  at(i): where state i is, in steps from ml and pu.
+  auto join = [&](int n, float4 s, const float4* ml, const float* pu, long long ml_step, long long u_step, auto at) {
+    const int most = __reduce_max_sync(0xffffffffu, n);  // the warp's rows go together
+    for (int i0 = 0; i0 < most; i0 += kLanes) {
+      if (i0 > 0) s = i0 + lane < n ? ml[at(i0 + lane) * ml_step] : none;
+      const bool some = s.y != 0.f;  // a state without a key may not even have its u; NaN is not 0
+      float m_new = some ? s.x : -INFINITY, mu_new = some ? s.z : -INFINITY;
+#pragma unroll
+      for (int x = kLanes / 2; x >= 1; x >>= 1) {
+        m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, x));
+        mu_new = fmaxf(mu_new, __shfl_xor_sync(0xffffffffu, mu_new, x));
+      }
+      m_new = fmaxf(m, m_new);
+      mu_new = fmaxf(mu, mu_new);
+      float share = some ? s.y * join_factor(s.x, m_new) : 0.f;
+#pragma unroll
+      for (int x = kLanes / 2; x >= 1; x >>= 1) share += __shfl_xor_sync(0xffffffffu, share, x);
+      l = l * join_factor(m, m_new) + share;
+      const float f = join_factor(mu, mu_new), g = join_factor(s.z, mu_new);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] *= f;
+      m = m_new;
+      mu = mu_new;
+      const unsigned has = __ballot_sync(0xffffffffu, some) >> (threadIdx.x % 32 / kLanes * kLanes);
+      for (int k0 = 0; k0 < min(kLanes, most - i0); k0 += kTogether) {
+        float4 v[kTogether][2];
+        float w[kTogether];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          const int i = k0 + k;
+          const bool take = (has >> i) & 1;
+          w[k] = __shfl_sync(0xffffffffu, g, i, kLanes);
+          if (!take) w[k] = 0.f;
+          const float4* from = reinterpret_cast<const float4*>(pu + at(i0 + i) * u_step);
+          v[k][0] = take ? from[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[k][1] = take ? from[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            u[4 * h] = fmaf(v[k][h].x, w[k], u[4 * h]);
+            u[4 * h + 1] = fmaf(v[k][h].y, w[k], u[4 * h + 1]);
+            u[4 * h + 2] = fmaf(v[k][h].z, w[k], u[4 * h + 2]);
+            u[4 * h + 3] = fmaf(v[k][h].w, w[k], u[4 * h + 3]);
+          }
+      }
+    }
+  };
   join(n_pre, pre_s, pre_ml, pre_u, kPrefixRows, (long long)kPrefixRows * D, pre_at);
   join(n_own, own_s, own_ml, own_u, p.cta_rows, (long long)p.cta_rows * D, own_at);
+  if constexpr (kGroups > 1) {
+    __shared__ float4 s_s[kBlockRows][kGroups];
+    __shared__ float4 s_u[kBlockRows][kGroups][2][kLanes];
+    if (lane == 0) s_s[in_block][group] = make_float4(m, l, mu, 0.f);
+    s_u[in_block][group][0][lane] = make_float4(u[0], u[1], u[2], u[3]);
+    s_u[in_block][group][1][lane] = make_float4(u[4], u[5], u[6], u[7]);
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int x = 1; x < kGroups; ++x) {
+      const float4 t = s_s[in_block][x];
+      if (t.y == 0.f) continue;
+      const float m_new = fmaxf(m, t.x), mu_new = fmaxf(mu, t.z);
+      l = l * join_factor(m, m_new) + t.y * join_factor(t.x, m_new);
+      const float f = join_factor(mu, mu_new), g = join_factor(t.z, mu_new);
+      const float* y = reinterpret_cast<const float*>(&s_u[in_block][x][0][lane]);
+      const float* z = reinterpret_cast<const float*>(&s_u[in_block][x][1][lane]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = u[e] * f + y[e] * g;
+        u[4 + e] = u[4 + e] * f + z[e] * g;
+      }
+      m = m_new;
+      mu = mu_new;
+    }
+  }
+  if (!valid) return;
   // l = 0: no key; NaN goes through
   const float f = l == 0.f ? 0.f : exp2f(mu - m);
+  uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) u[e] = l == 0.f ? 0.f : u[e] / l * f;
-  store_row<E>(static_cast<T*>(a.o) + row * D + lane * E, u);
+  for (int e = 0; e < 8; ++e) u[e] = l == 0.f ? 0.f : u[e] / l * f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = ptx::pack16x2<std::is_same<T, __half>::value>(u[2 * e], u[2 * e + 1]);
+  *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * D + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
   if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T>
 cudaError_t launch_merge(const MergeParams& p, int D, cudaStream_t s) {
   const long long rows = (long long)p.a.B * p.a.Hk * p.a.group * p.a.nq;
-  const int ctas = (int)((rows + kMergeWarps - 1) / kMergeWarps);
+  // states of a row, about: the prefix's parts, and the CTAs that share a unit of the own rows
+  const long long units = (long long)p.a.B * p.a.Hk * p.row_groups;
+  const long long states = (p.a.np > 0 ? (p.pre.steps / p.pre.per_cta + 1) * (p.pre.split ? 2 : 1) : 0) + kOwnCtas / units;
+  const bool few = rows <= kFewRows && states >= kManyStates;
+  const int per = kMergeThreads / (D / 8) / (few ? 4 : 1);
+  auto* kernel = few ? (D == 64 ? merge_kernel<T, 64, 4> : merge_kernel<T, 128, 4>)
+                     : (D == 64 ? merge_kernel<T, 64, 1> : merge_kernel<T, 128, 1>);
   return note_error("cached decoding merge launch",
-                    launch_serve_kernel(D == 64 ? merge_kernel<T, 64> : merge_kernel<T, 128>, ctas, kMergeWarps * 32, 0,
+                    launch_serve_kernel(kernel, (int)((rows + per - 1) / per), kMergeThreads, 0,
                                         p.a.np > 0 || p.a.max_len > 0, s, p));
 }
 

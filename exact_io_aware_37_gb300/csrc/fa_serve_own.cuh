@@ -512,38 +512,43 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += C::kChunk) {
             if (r0 >= valid) break;
+            // The chunk's weights first, its stores last: a store of bytes may alias what the next
+            // row would read, and the rows' chains of conversions would run one after another.
             float v[C::kChunk];
+            uint32_t t[C::kChunk / 2][C::kTerms];
             read_chunk(at_s + r0, v);
+#pragma unroll
+            for (int e = 0; e < C::kChunk; ++e) {
+              const RowInfo info = row[r0 + e];
+              const float f = info.factor * kf;
+              const bool hidden = at_edge.value && key >= info.limit;
+              if constexpr (C::kCodes)
+                l[r0 + e] += ex2_approx(hidden ? -INFINITY : fmaf(v[e], f, info.neg_l));
+              v[e] = ex2_approx(hidden ? -INFINITY : fmaf(v[e], f, info.neg_w + ve));
+              if constexpr (!C::kCodes) l[r0 + e] += v[e];  // the unrounded weights
+            }
+#pragma unroll
+            for (int e = 0; e < C::kChunk; e += 2) {
+              if constexpr (C::kCodes)
+                c8::encode2_terms(__floats2half2_rn(v[e], v[e + 1]), t[e / 2]);
+              else
+                t[e / 2][0] = pack16x2<Kind == kF16>(v[e], v[e + 1]);
+            }
 #pragma unroll
             for (int e = 0; e < C::kChunk; e += 2) {
               const int r = r0 + e;
               if (r >= valid) break;
-              float x[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const RowInfo info = row[r + y];
-                const float f = info.factor * kf;
-                const bool hidden = at_edge.value && key >= info.limit;
-                x[y] = ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_w + ve));
-                if constexpr (C::kCodes)
-                  l[r + y] += ex2_approx(hidden ? -INFINITY : fmaf(v[e + y], f, info.neg_l));
-                else
-                  l[r + y] += x[y];  // the unrounded weights
-              }
               if constexpr (C::kCodes) {
-                uint32_t t[3];
-                c8::encode2_terms(__floats2half2_rn(x[0], x[1]), t);
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                   const int at = k * R + r;
-                  sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[k];
-                  sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[k] >> 8);
+                  sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[e / 2][k];
+                  sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[e / 2][k] >> 8);
                 }
               } else {
-                const uint32_t t = pack16x2<Kind == kF16>(x[0], x[1]);
                 uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
-                *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t;
-                *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t >> 16);
+                *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t[e / 2][0];
+                *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t[e / 2][0] >> 16);
               }
             }
           }
