@@ -45,12 +45,12 @@ __device__ __forceinline__ int own_cost(const ServeArgs& a, int tiles) { return 
 __device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }
 
 // A CTA's share [first, end) of the cost of all sequences laid out in a row
-// (sequence-major, units of a sequence, in a unit the run's own cost and then its tiles); `base`
-// lies before sequence b, which holds position `first`.  A tile belongs to the CTA whose
-// share its position falls into.
+// (sequence-major, units -- key head, row group -- of a sequence, in a unit the run's own cost and then its
+// tiles).  Position `first` is `off` into unit (b, hk, rg).  A tile belongs to the CTA
+// whose share its position falls into.
 struct OwnPlan {
-  long long first, end, base;
-  int b;
+  long long first, end;
+  int b, hk, rg, off;
 };
 
 // Works out the CTA's share.  Block-wide; the caller's shared memory may be
@@ -58,9 +58,10 @@ struct OwnPlan {
 // leaves the layout for the merge kernel: a.plan[0] = a CTA's share, a.plan[1 + b] = what
 // lies before sequence b.
 template <int kThreads>
-__device__ __forceinline__ void own_plan(const ServeArgs& a, int units, OwnPlan& plan) {
+__device__ __forceinline__ void own_plan(const ServeArgs& a, int row_groups, OwnPlan& plan) {
   __shared__ long long s_sum[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long units = (long long)a.Hk * row_groups;  // of one sequence
   auto cost = [&](int b) -> long long {
     if (b >= a.B) return 0;
     const int len = raw_len(a, b);
@@ -107,8 +108,11 @@ __device__ __forceinline__ void own_plan(const ServeArgs& a, int units, OwnPlan&
       before += s_sum[i];
     }
     if (b < a.B && at <= first && first < at + n) {
-      plan.base = at;
+      const long long unit_cost = n / units, unit = (first - at) / unit_cost;
       plan.b = b;
+      plan.hk = (int)(unit / row_groups);
+      plan.rg = (int)(unit - (long long)plan.hk * row_groups);
+      plan.off = (int)(first - at - unit * unit_cost);
     }
     if (blockIdx.x == 0 && b < a.B) a.plan[1 + b] = at;
   }

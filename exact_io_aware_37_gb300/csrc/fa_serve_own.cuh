@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   const ServeArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = a.group * a.nq;
-  const int units = a.Hk * p.row_groups;  // of one sequence
 
   if (threadIdx.x == 0) {
     for (unsigned s = 0; s < H; ++s) {
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     tmem_relinquish();
   }
   tc_fence_before();
-  own_plan<kOwnThreads>(a, units, plan);  // holds block-wide barriers
+  own_plan<kOwnThreads>(a, p.row_groups, plan);  // holds block-wide barriers
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem = tmem_base_sh;
@@ -226,37 +225,38 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     int len, row0, slab, tile0, n;
     bool ends;  // the run holds the unit's last tile
   };
-  struct Walk {
-    long long t, base;
-    int b;
+  struct Walk {  // the next unit, and where in its cost the share goes on (0 but for the first)
+    long long t;
+    int b, hk, rg, off;
   };
   auto next_run = [&](Walk& k, Run& q) -> bool {
     while (k.t < plan.end) {
       q.len = seq_len(a, k.b);
       const int nt = own_tiles(q.len), cost = own_cost(a, nt);
-      const long long here = (long long)cost * units;
-      if (k.t >= k.base + here) {
-        k.base += here;
+      if (cost == 0) {  // an empty sequence
         ++k.b;
         continue;
       }
-      const long long at = k.t - k.base;
-      const int unit = (int)(at / cost);
-      const int x0 = (int)(at - (long long)unit * cost);
-      const int x1 = (int)min((long long)cost, x0 + (plan.end - k.t));
+      const int x0 = k.off, x1 = (int)min((long long)cost, x0 + (plan.end - k.t));
       k.t += x1 - x0;
       q.tile0 = max(0, x0 - a.run_cost);
       q.n = max(0, x1 - a.run_cost) - q.tile0;
-      if (q.n <= 0) continue;  // the share ends before the unit's first tile
       q.ends = x1 == cost;
-      const int hk = unit / p.row_groups;
-      q.row0 = (unit - hk * p.row_groups) * R;
-      q.slab = k.b * a.Hk + hk;
-      return true;
+      q.row0 = k.rg * R;
+      q.slab = k.b * a.Hk + k.hk;
+      k.off = 0;
+      if (++k.rg == p.row_groups) {
+        k.rg = 0;
+        if (++k.hk == a.Hk) {
+          k.hk = 0;
+          ++k.b;
+        }
+      }
+      if (q.n > 0) return true;  // else the share ended before the unit's first tile
     }
     return false;
   };
-  Walk walk{plan.first, plan.base, plan.b};
+  Walk walk{plan.first, plan.b, plan.hk, plan.rg, plan.off};
 
   if (warp < 4) {
     // ------------------------------------------------------------ softmax
