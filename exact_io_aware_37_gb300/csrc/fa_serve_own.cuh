@@ -22,9 +22,9 @@
 // by warp-level MMA were tried first: about 60 cycles each a warp on this part, so eight
 // warps an SM held the step at 239 us, B16 H32 8192 keys D128, floor 159.)
 //
-// Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile's
-// references hold unless some score outgrows them, which a first look at the scores and one barrier with
-// a vote find out; the threads write P^T as the second product's narrow operand, one byte
+// Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile is
+// weighed with the references as they are; only if some score outgrew them, which one
+// barrier with a vote finds out, are new ones found and the tile weighed again.  The threads write P^T as the second product's narrow operand, one byte
 // (or 16-bit value) a row and term, and read O^T at a run's end, by when the next run's queries are in
 // place.  Warp 4: TMA producer; K and V tiles share one ring that runs on over a CTA's
 // runs.  Warp 5: MMA issuer; S^T of the next tile is issued before the softmax of this one is done.
@@ -54,7 +54,7 @@ constexpr int kBoxKeys = 32;  // keys of one TMA box: a last tile reads no more 
 // they stay within 256 and the terms reach down to 2^-20 / 2^4 = 2^-24 of the reference (fp16:
 // 2^-25).  A slack of 2^1 at a scale of 2^7 found new references in every other tile
 // at 20 rows a key head (172 us against 90, 24 ragged sequences up to 16384 keys).
-constexpr float kWeightLog2 = 4.f;
+constexpr float kWeightLog2 = 4.f;  // codes only
 constexpr float kRefSlack = 4.f;   // log2 units a weight may outgrow its reference by
 constexpr float kSumSlack = 60.f;  // the same for the float32 normaliser
 
@@ -157,20 +157,19 @@ __device__ __forceinline__ void sum_rows(float (&l)[R], int lane) {
 // What the threads share about a query row of a run.
 struct RowInfo {
   float factor;        // from products to log2 units
-  float neg_w, neg_l;  // minus the references (0 without a key so far; neg_w holds the weights' scale)
+  float neg_w, neg_l;  // minus the references (neg_w holds the weights' scale)
   int limit;           // keys it sees
 };
-struct RowTest {
-  float factor;
-  float most_w, most_l;  // what the references allow
-  int limit;
-};
+// In place of minus a reference while a row has seen no score above -inf: any such score
+// outgrows it.
+constexpr float kNoReference = 1e30f;
 
 template <int Kind, int D, int R>
 __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_kernel(
     const __grid_constant__ OwnParams p) {
   using C = OwnCfg<Kind, D, R>;
   constexpr unsigned H = C::kSlots;
+  constexpr float kWeightScale = C::kCodes ? kWeightLog2 : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // Steps (tiles) g are counted over all of a CTA's runs.  full / free: the ring; bar_s[g % 2]:
@@ -181,9 +180,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   __shared__ __align__(8) uint64_t bar_s[2], bar_p, bar_o, bar_q, bar_done;
   // by the run's parity: the next run's are written while this one's are in use
   __shared__ __align__(16) RowInfo s_row[2][R];
-  __shared__ __align__(16) RowTest s_test[2][R];
   __shared__ float s_refw[2][R], s_refl[2][R];  // references of the weights and of the normaliser
-  __shared__ float s_mw[4][R], s_ml[4][R];      // warps' maxima, and sums at a run's end
+  __shared__ float s_mw[4][R], s_ml[4][R];      // warps' maxima
+  __shared__ float s_sum[4][R];                 // and sums, at a run's end
   __shared__ float s_fw[R], s_fl[R];            // rescaling
   __shared__ int s_bad[2];
   __shared__ OwnPlan plan;
@@ -326,8 +325,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           // a row past the last weighs nothing and outgrows nothing
           const bool there = r < valid;
           const int limit = a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len;
-          s_row[par][r] = RowInfo{factor, there ? 0.f : -INFINITY, there ? 0.f : -INFINITY, limit};
-          s_test[par][r] = RowTest{factor, there ? -INFINITY : INFINITY, there ? -INFINITY : INFINITY, limit};
+          s_row[par][r] = RowInfo{factor, there ? kNoReference : -INFINITY, there ? kNoReference : -INFINITY, limit};
           s_refw[par][r] = s_refl[par][r] = there ? -INFINITY : INFINITY;
         }
       }
@@ -398,27 +396,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         tc_fence_after();
         const uint32_t at_s = t_s + (g & 1) * C::kN;
         const bool edge = key0 + kOwnTile > lim_all;
-        // ---- do the references hold?
-        bool over = false;
-        auto look = [&](auto at_edge) {
-#pragma unroll
-          for (int r0 = 0; r0 < R; r0 += C::kChunk) {
-            if (r0 >= valid) break;
-            float v[C::kChunk];
-            read_chunk(at_s + r0, v);
-#pragma unroll
-            for (int e = 0; e < C::kChunk; ++e) {
-              const RowTest t = s_test[par][r0 + e];
-              const float x = v[e] * (t.factor * kf);
-              const bool more = x > (C::kCodes ? fminf(t.most_w - ve, t.most_l) : t.most_w);
-              over |= at_edge.value ? more && key < t.limit : more;
-            }
-          }
-        };
-        if (edge)
-          look(Flag<true>{});
-        else
-          look(Flag<false>{});
         // At the edge: values of keys past the end become zero, and so do those that are
         // not finite of keys that only some rows see (0 * NaN would reach the rows that
         // do not); the rows that do see them get them at the run's end.
@@ -444,13 +421,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
                 }
               }
         }
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        bool o_done = i == 0;
-        if (named_bar_or(1, 128, over || !ok)) {
-          if (!named_bar_and(1, 128, ok)) {
-            ok = false;
-            break;
-          }
+        // Finds the rows' references again: false when some warp has given up.
+        auto refer = [&]() -> bool {
 #pragma unroll 1
           for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
             float v[C::kChunk];
@@ -466,7 +438,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
               }
             }
           }
-          named_bar_sync(1, 128);
+          if (!named_bar_and(1, 128, ok)) return false;
           if (tid < valid) {
             auto grow = [](float& ref, float m0, float m1, float m2, float m3) {
               const float m = fmaxf(ref, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
@@ -476,39 +448,19 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             };
             s_fw[tid] = grow(s_refw[par][tid], s_mw[0][tid], s_mw[1][tid], s_mw[2][tid], s_mw[3][tid]);
             s_fl[tid] = grow(s_refl[par][tid], s_ml[0][tid], s_ml[1][tid], s_ml[2][tid], s_ml[3][tid]);
-            // a row without a key so far (or with -inf scores alone) has reference 0
             const float rw = s_refw[par][tid], rl = s_refl[par][tid];
-            s_row[par][tid].neg_w = (C::kCodes ? kWeightLog2 : 0.f) - (rw == -INFINITY ? 0.f : rw);
-            s_row[par][tid].neg_l = rl == -INFINITY ? 0.f : -rl;
-            s_test[par][tid].most_w = rw + kRefSlack;
-            s_test[par][tid].most_l = rl + kSumSlack;
+            s_row[par][tid].neg_w = rw == -INFINITY ? kNoReference : kWeightScale - rw;
+            s_row[par][tid].neg_l = rl == -INFINITY ? kNoReference : -rl;
           }
           named_bar_sync(1, 128);
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (r < valid) l[r] *= s_fl[r];
-          if (i > 0) {
-            ok = warp_wait(&bar_o, (g - 1) & 1, w);
-            o_done = true;
-            tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < C::kTerms; ++k)
-#pragma unroll 1
-              for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
-                uint32_t o[C::kChunk];
-                tmem_ld(t_o + k * R + r0, o);
-                tmem_ld_wait(o);
-#pragma unroll
-                for (int e = 0; e < C::kChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_fw[r0 + e]);
-                tmem_st(t_o + k * R + r0, o);
-              }
-            tmem_st_wait();
-            tc_fence_before();
-          }
-        }
-        // ---- weights: P^T's place is free once the step before has been added
-        if (!o_done) ok = warp_wait(&bar_o, (g - 1) & 1, w);
-        auto weigh = [&](auto at_edge) {
+          return true;
+        };
+        // Weighs the tile.  kFirst: adds to the sums (unrounded weights) and says whether some
+        // score outgrew its reference.  Again, under new references: the sums, rescaled, hold
+        // the tile already, but where the old reference let a weight overflow; what was there before
+        // is then nothing beside it.
+        auto weigh = [&](auto at_edge, auto first) -> bool {
+          float most_w = -INFINITY, most_l = -INFINITY;
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += C::kChunk) {
             if (r0 >= valid) break;
@@ -522,10 +474,20 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
               const RowInfo info = row[r0 + e];
               const float f = info.factor * kf;
               const bool hidden = at_edge.value && key >= info.limit;
-              if constexpr (C::kCodes)
-                l[r0 + e] += ex2_approx(hidden ? -INFINITY : fmaf(v[e], f, info.neg_l));
-              v[e] = ex2_approx(hidden ? -INFINITY : fmaf(v[e], f, info.neg_w + ve));
-              if constexpr (!C::kCodes) l[r0 + e] += v[e];  // the unrounded weights
+              const float x = hidden ? -INFINITY : fmaf(v[e], f, info.neg_w + ve);
+              float sum = 0.f;
+              if constexpr (C::kCodes) {
+                const float y = hidden ? -INFINITY : fmaf(v[e], f, info.neg_l);
+                sum = ex2_approx(y);
+                if (first.value) most_l = fmaxf(most_l, y);
+              }
+              if (first.value) most_w = fmaxf(most_w, x);
+              v[e] = ex2_approx(x);
+              if constexpr (!C::kCodes) sum = v[e];
+              if (first.value)
+                l[r0 + e] += sum;
+              else if (l[r0 + e] == INFINITY)
+                l[r0 + e] = sum;
             }
 #pragma unroll
             for (int e = 0; e < C::kChunk; e += 2) {
@@ -552,11 +514,45 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
               }
             }
           }
+          return most_w > kWeightScale + kRefSlack || most_l > kSumSlack;
         };
-        if (edge)
-          weigh(Flag<true>{});
-        else
-          weigh(Flag<false>{});
+        auto weigh_tile = [&](auto first) { return edge ? weigh(Flag<true>{}, first) : weigh(Flag<false>{}, first); };
+
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (i == 0) {
+          if (!refer()) {
+            ok = false;
+            break;
+          }
+          weigh_tile(Flag<true>{});
+        } else {
+          // P^T's place is free, and O^T at rest, once the step before has been added
+          ok = ok && warp_wait(&bar_o, (g - 1) & 1, w);
+          tc_fence_after();
+          const bool over = weigh_tile(Flag<true>{});
+          if (named_bar_or(1, 128, over || !ok)) {
+            if (!refer()) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (r < valid && l[r] != INFINITY) l[r] *= s_fl[r];
+#pragma unroll 1
+            for (int k = 0; k < C::kTerms; ++k)
+#pragma unroll 1
+              for (int r0 = 0; r0 < valid; r0 += C::kChunk) {
+                uint32_t o[C::kChunk];
+                tmem_ld(t_o + k * R + r0, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < C::kChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_fw[r0 + e]);
+                tmem_st(t_o + k * R + r0, o);
+              }
+            tmem_st_wait();
+            weigh_tile(Flag<false>{});
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -603,10 +599,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       // (lanes that share a row hold equal sums).
       sum_rows<R>(l, lane);
       constexpr int kRows2 = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
-      if (lane < R && lane < kRows2) s_ml[warp][lane] = l[0];
+      if (lane < R && lane < kRows2) s_sum[warp][lane] = l[0];
       named_bar_sync(1, 128);
       if (tid < valid)
-        slot.ml[tid] = make_float4(s_refl[par][tid], s_ml[0][tid] + s_ml[1][tid] + s_ml[2][tid] + s_ml[3][tid],
+        slot.ml[tid] = make_float4(s_refl[par][tid], s_sum[0][tid] + s_sum[1][tid] + s_sum[2][tid] + s_sum[3][tid],
                                    s_refw[par][tid], 0.f);
       tc_fence_before();
       q = nx;

@@ -170,12 +170,17 @@ def run_own(runs, seed, H=3, W=3, skip=()):
                 yield from maybe("s", wait(s[g & 1], g >> 1))
                 assert m.has.get(("S", g & 1, w)) == g, "scores of another step"
                 yield
-                yield from meet.come()  # the vote
-                if i > 0:
+                if i == 0:  # references, then the weights
+                    yield from meet.come()
+                    yield from meet.come()
+                else:
                     yield from maybe("o", wait(o, g - 1))
-                assert m.has.get(("S", g & 1, w)) == g, "scores overwritten while in use"
-                m.write(("P", w), g)
-                yield
+                for again in range(1 + (i > 0)):
+                    assert m.has.get(("S", g & 1, w)) == g, "scores overwritten while in use"
+                    m.write(("P", w), g)
+                    yield
+                    if i > 0 and not again:
+                        yield from meet.come()  # the vote; then perhaps once more
                 p.arrive()
                 g += 1
             yield from meet.come()
