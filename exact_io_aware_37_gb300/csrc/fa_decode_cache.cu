@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
   const int len = raw_len(a, b);
   const bool valid = there && len_ok(a, len);
+  if (there && !valid && lane == 0 && group == 0) atomicOr(a.status, kDevBadSeqlens);
   const int nt = valid ? own_tiles(len) : 0, rg = r / p.cta_rows;
   if (!valid) n_pre = 0;
   ptx::grid_wait();

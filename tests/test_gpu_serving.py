@@ -222,12 +222,19 @@ CACHE = [
     (5, 3, 3, 2, 63, [0, 1, 2, 63, 31], 128, BF16, True),
     (1, 40, 1, 5, 257, [256], 64, F16, True),                           # 200 rows
     (1, 2, 1, 1, 40000, [39999], 128, BF16, True),
+    (2, 3, 1, 8, 300, [300, 129], 64, BF16, True),                      # 24 rows
+    (1, 4, 1, 5, 1000, [1000], 128, BF16, True),                        # 20 rows
+    (1, 4, 2, 70, 500, [333], 128, F16, True),                          # a piece of a prompt: 140 rows
+    (300, 2, 1, 1, 40, None, 64, F16, True),                            # more sequences than a block plans at once
+    (3, 2, 2, 1, 1500, [1500, 0, 1409], 64, BF16, True),
 ]
 
 
 @pytest.mark.parametrize("case", CACHE, ids=name)
 def test_decode_cache_matches_the_reference(case):
     B, H, Hk, nq, cap, lens, D, dtype, causal = case
+    if lens is None:
+        lens = [int(x) for x in synth.varlen_lengths(B, 0, cap, 8)]
     c = random_cache(B, Hk, cap, D, 100)
     q = (synth.normal((B, H, nq, D), 103, F32) * 2).to(dtype).to(DEV)
     o, lse = outputs(q)
@@ -256,6 +263,13 @@ SHARED = [
     (4, 6, 2, 3, 256, 40, [9, 40, 0, 2], 128, F16, False, True),        # not causal
     (16, 5, 1, 1, 20000, 128, None, 128, BF16, True, True),
     (129, 1, 1, 1, 128, 5, None, 64, F16, True, False),
+    (2, 5, 1, 2, 200, 300, [300, 129], 128, BF16, True, False),         # 16-bit rows: 10, 24, 20, 15 rows a key head
+    (2, 6, 1, 4, 200, 300, [257, 31], 128, F16, True, False),
+    (2, 4, 1, 5, 200, 400, [400, 64], 64, BF16, True, False),
+    (3, 15, 1, 1, 1, 700, [700, 0, 128], 64, F16, False, False),
+    (2, 9, 3, 40, 384, 260, [260, 40], 128, BF16, True, False),         # 120 rows a key head
+    (300, 4, 2, 1, 130, 6, None, 128, F16, True, True),                 # 600 rows, little of their own
+    (7, 2, 2, 1, 128 * 153, 20, None, 64, BF16, True, True),            # one unit over all CTAs, and then some
 ]
 
 
@@ -373,12 +387,56 @@ def test_queries_of_any_size(magnitude):
     check(o, lse, reference(q, None, None, c, [cap], float(np.float32(scale)), True), cap, F16, 64.0)
 
 
+@pytest.mark.parametrize("own8", [True, False])
+def test_scores_that_rise_along_the_cache(own8):
+    """Every tile's scores above the last one's by less than, about, and far more than
+    what a reference allows; then by more than float32's exponents reach."""
+    D, cap = 128, 1300
+    q = torch.zeros(1, 3, 1, D, dtype=BF16)
+    q[..., 0] = 1.0
+    for step in (0.5, 3.0, 2.5 * np.log(2) * 4, 60.0, 400.0):
+        k = torch.zeros(1, 1, cap, D)
+        k[..., 0] = (torch.arange(cap) // 100 * step)
+        v = synth.normal((1, 1, cap, D), 157, F32)
+        if own8:
+            c = fa.cache_alloc(1, 1, cap, D)
+            fa.fa_cache_write(k.to(DEV), v.to(DEV), c)
+        else:
+            c = tuple(x.to(BF16).to(DEV) for x in (k, v))
+        kp, vp = (torch.zeros(1, 0, D, dtype=BF16, device=DEV) for _ in range(2))
+        o, lse = fa.decode_shared(q.to(DEV), kp, vp, c, scale=1.0)
+        assert ok()
+        want = reference(q, None, None, c, [cap], 1.0, True)
+        check(o, lse, want, cap, F16 if own8 else BF16, 8.0)
+
+
+def test_infinite_scores_weigh_nothing_or_everything():
+    """-inf in a 16-bit key: as if it were not there; a row of nothing else is not a number,
+    as in the definition (0 / 0)."""
+    D, cap = 64, 300
+    q = torch.zeros(1, 1, 1, D, dtype=BF16)
+    q[..., 0] = 1.0
+    k, v = (synth.normal((1, 1, cap, D), 158 + i, BF16) for i in range(2))
+    kp, vp = (torch.zeros(1, 0, D, dtype=BF16, device=DEV) for _ in range(2))
+    k[0, 0, :200, 0] = float("-inf")                                    # whole first tile, part of the second
+    o, lse = fa.decode_shared(q.to(DEV), kp, vp, (k.to(DEV), v.to(DEV)), scale=1.0)
+    assert ok()
+    tail = tuple(x[:, :, 200:].contiguous() for x in (k, v))
+    check(o, lse, reference(q, None, None, tail, [100], 1.0, True), 100, BF16, 8.0)
+
+
 def test_lengths_out_of_range_are_skipped_and_reported():
     B, H, Hk, nq, np_, cap, D = 4, 2, 1, 2, 33, 20, 64
     q = synth.normal((B, H, nq, D), 160, BF16).to(DEV)
     kp, vp = (synth.normal((Hk, np_, D), 161 + i, BF16).to(DEV) for i in range(2))
     c = random_cache(B, Hk, cap, D, 163)
     good = fa.decode_shared(q, kp, vp, c, int32([20, 3, 5, 1]))
+    none = tuple(torch.empty(B, Hk, 0, D, dtype=BF16, device=DEV) for _ in range(2))  # no rows of their own at all
+    o, lse = torch.full_like(q, 9.0), torch.full((B, H, nq), 9.0, device=DEV)
+    fa.fa_decode_shared(q, kp, vp, none, int32([0, 1, 0, -1]), o, lse, True)
+    torch.cuda.synchronize()
+    assert fa.fa_get_last_device_error() == -1
+    assert bool((o[1::2] == 9.0).all()) and bool((lse[1::2] == 9.0).all()) and not bool((lse[::2] == 9.0).any())
     for bad in (-1, 21, 2 ** 31 - 1, -2 ** 31):
         o, lse = torch.full_like(q, 9.0), torch.full((B, H, nq), 9.0, device=DEV)
         fa.fa_decode_shared(q, kp, vp, c, int32([20, bad, 5, 1]), o, lse, True)
