@@ -64,7 +64,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
   const int len = raw_len(a, b);
   const bool valid = there && len_ok(a, len);
-  if (there && !valid && lane == 0 && group == 0) atomicOr(a.status, kDevBadSeqlens);
   const int nt = valid ? own_tiles(len) : 0, rg = r / p.cta_rows;
   if (!valid) n_pre = 0;
   ptx::grid_wait();
@@ -181,7 +180,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       mu = mu_new;
     }
   }
-  if (!valid) return;
+  if (!valid) {
+    if (there && lane == 0) atomicOr(a.status, kDevBadSeqlens);
+    return;
+  }
   // l = 0: no key; NaN goes through
   const float f = l == 0.f ? 0.f : exp2f(mu - m);
   uint32_t w[4];

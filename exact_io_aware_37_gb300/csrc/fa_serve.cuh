@@ -29,7 +29,7 @@ inline int own_rows(int rows) {
   return (rows + 15) / 16 <= (rows + 23) / 24 ? 16 : 24;  // the fewest groups, then the fewest rows
 }
 
-// A length out of range counts as 0 (the join reports it and leaves its rows alone).
+// A length out of range counts as 0 (reported here and by the join, which leaves its rows alone).
 __device__ __forceinline__ int raw_len(const ServeArgs& a, int b) { return a.lens ? __ldg(a.lens + b) : a.max_len; }
 __device__ __forceinline__ bool len_ok(const ServeArgs& a, int len) { return len >= 0 && len <= a.max_len; }
 __device__ __forceinline__ int seq_len(const ServeArgs& a, int b) {
@@ -64,7 +64,12 @@ __device__ __forceinline__ void own_plan(const ServeArgs& a, int row_groups, Own
   const long long units = (long long)a.Hk * row_groups;  // of one sequence
   auto cost = [&](int b) -> long long {
     if (b >= a.B) return 0;
-    return (long long)own_cost(a, own_tiles(seq_len(a, b))) * units;
+    const int len = raw_len(a, b);
+    if (!len_ok(a, len)) {
+      if (blockIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
+      return 0;
+    }
+    return (long long)own_cost(a, own_tiles(len)) * units;
   };
   const long long mine = cost(threadIdx.x);  // the first kThreads sequences: enough for most batches
   long long x = mine;
