@@ -516,7 +516,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           }
           return most_w > kWeightScale + kRefSlack || most_l > kSumSlack;
         };
-        auto weigh_tile = [&](auto first) { return edge ? weigh(Flag<true>{}, first) : weigh(Flag<false>{}, first); };
+        auto weigh_tile = [&](auto first) {  // (a second weighing is rare: one form of it will do)
+          return edge || !first.value ? weigh(Flag<true>{}, first) : weigh(Flag<false>{}, first);
+        };
 
         ok = __all_sync(0xffffffffu, ok) != 0;
         if (i == 0) {

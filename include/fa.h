@@ -424,8 +424,8 @@ fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t*
  *         are never used, whatever they hold
  *   o     [B, H, nq, D] written (dtype);  lse [B, H, nq] float32, natural log
  * Query row i sits at position lens[b] - nq + i, so causal allows key j iff j <= i + lens[b] - nq.  Rows with no
- * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32; the weights are rounded to
- * fp16 for their product with the values.
+ * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32; for its product with the
+ * value a weight is rounded to fp16's 11 bits, down to 2^-24 of the largest contribution's.
  * workspace: DEVICE scratch of fa_decode_cache_workspace_size(...) bytes, 256-byte aligned, owned by the caller; its
  * contents do not matter; calls (and graph replays) that overlap on the GPU need workspaces of their own. */
 size_t fa_decode_cache_workspace_size(int B, int H, int Hk, int nq, int max_len, int D, fa_dtype dtype);
