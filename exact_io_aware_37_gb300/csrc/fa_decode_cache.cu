@@ -5,8 +5,8 @@
 // queries sits at position total - nq + i of its sequence's total = np + len
 // keys, so causal allows key j iff j <= i + total - nq.
 //
-// A step is up to three launches: the pass over the own rows (fa_serve_own.cuh), the
-// pass over the prefix (fa_tc_prefix.cu), and the join of the states they
+// A step is up to three launches: the pass over the prefix (fa_tc_prefix.cu), the
+// pass over the own rows (fa_serve_own.cuh), beside it, and the join of the states they
 // leave, here: m = max m_s, l = sum l_s 2^(m_s - m), u = sum u_s 2^(mu_s - mu),
 // O = u 2^(mu - m) / l, L = (m + log2 l) ln 2.  Each launch may start while the one
 // in front of it drains.
@@ -246,7 +246,13 @@ size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, 
   a.nq = nq;
   a.np = np;
   a.max_len = max_len;
-  return carve(a, D, prefix_plan(B, Hk, a.group * nq, np), nullptr);
+  // the layout depends on whether the own rows are 8-bit; the size covers both
+  size_t most = 0;
+  for (int elem = 1; elem <= 2; ++elem) {
+    const size_t bytes = carve(a, D, serve_plan(B, Hk, a.group * nq, np, max_len, D, elem).pre, nullptr);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s) {
@@ -255,12 +261,14 @@ cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cuda
   MergeParams m;
   m.cta_rows = own_rows(a.group * a.nq);
   m.row_groups = (a.group * a.nq + m.cta_rows - 1) / m.cta_rows;
-  m.pre = prefix_plan(a.B, a.Hk, a.group * a.nq, a.np);
+  const ServePlan plan = serve_plan(a.B, a.Hk, a.group * a.nq, a.np, a.max_len, D, a.k_exp ? 1 : 2);
+  m.pre = plan.pre;
   carve(a, D, m.pre, static_cast<char*>(workspace));
   cudaError_t e = cudaSuccess;
-  // The own rows first: where their shares end unevenly the prefix's CTAs, all alike, move in.
-  if (a.max_len > 0) e = a.k_exp ? launch_own_e4m3(a, D, f16, s) : launch_own_16(a, D, f16, s);
-  if (e == cudaSuccess && a.np > 0) e = launch_prefix(a, m.pre, D, f16, a.max_len > 0, s);
+  if (a.np > 0) e = launch_prefix(a, m.pre, D, f16, s);
+  if (e == cudaSuccess && a.max_len > 0)
+    e = a.k_exp ? launch_own_e4m3(a, D, f16, plan.own_sms, plan.together, s)
+                : launch_own_16(a, D, f16, plan.own_sms, plan.together, s);
   if (e != cudaSuccess) return e;
   m.a = a;
   return f16 ? launch_merge<__half>(m, D, s) : launch_merge<__nv_bfloat16>(m, D, s);

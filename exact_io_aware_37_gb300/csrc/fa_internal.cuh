@@ -221,10 +221,10 @@ struct ServeArgs {
   float4* pre_ml;
 };
 struct PrefixPlan;
-// The pass over the sequences' own rows, and the one over the prefix (`after`: in its wake).
-cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, cudaStream_t s);
-cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, cudaStream_t s);
-cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, bool after, cudaStream_t s);
+// The pass over the prefix, and the one over the sequences' own rows on `sms` SMs (`after`: beside the prefix).
+cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, cudaStream_t s);
+cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, int sms, bool after, cudaStream_t s);
+cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, int sms, bool after, cudaStream_t s);
 size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, int D);
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s);
 

@@ -11,10 +11,11 @@
 
 namespace fa {
 
-// The pass over the own rows (fa_serve_own.cuh): at most two CTAs on each of 152
-// SMs.  Nothing depends on how many run at once, and the workspace's size must not
-// depend on the device.
-constexpr int kOwnCtas = 304;
+// SMs the work is cut for.  Nothing depends on how many there are or on what runs at
+// once, and the workspace's size must not depend on the device.
+constexpr int kSms = 152;
+// The pass over the own rows (fa_serve_own.cuh): at most two CTAs an SM.
+constexpr int kOwnCtas = 2 * kSms;
 constexpr int kOwnTile = 128;  // keys of a step
 // What a run costs besides its tiles (queries in, references found, state out), in tiles: it
 // only steers the cut.  About as long as 96 KB of cache take: fitted over the CTAs of
@@ -135,16 +136,15 @@ __device__ __forceinline__ PartSlot own_slot(const ServeArgs& a, int cta, bool b
 
 // The pass over the prefix (fa_tc_prefix.cu): units of kPrefixRows (split) or
 // 2 kPrefixRows query rows of a key head, each of `steps` tiles of kPrefixKeys keys;
-// all units' steps in a row, per_cta of them a CTA.
+// all units' steps in a row, per_cta of them a CTA, a CTA an SM.
 constexpr int kPrefixRows = 128, kPrefixKeys = 128;
-constexpr int kPrefixCtas = 152;  // one an SM; a constant for the workspace's sake, as above
 struct PrefixPlan {
   int split;              // at most kPrefixRows rows: the two slots share them and halve the keys
   int pairs, steps, units;
   int ctas, parts;        // parts: states kept for a unit (CTAs that may share it)
   long long per_cta;
 };
-inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np) {
+inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
   PrefixPlan p;
   const long long rows = (long long)B * gq;
   p.split = rows <= kPrefixRows;
@@ -152,10 +152,51 @@ inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np) {
   p.steps = (np + kPrefixKeys - 1) / kPrefixKeys;
   p.units = p.pairs * Hk;
   const long long all = (long long)p.units * p.steps;
-  p.per_cta = (all + kPrefixCtas - 1) / kPrefixCtas;
+  p.per_cta = (all + ctas - 1) / ctas;
   p.ctas = p.per_cta > 0 ? (int)((all + p.per_cta - 1) / p.per_cta) : 0;
   p.parts = p.per_cta > 0 ? (int)((p.steps - 1) / p.per_cta) + 2 : 0;
   return p;
+}
+
+// How a step is laid over the SMs.  With a prefix and own rows, the two passes run
+// side by side, the prefix on as many SMs as let both end at about the same time: each pass's
+// start and end (its queries, first copies, states) hides behind the other's stream.  64 sequences behind 8192 keys,
+// 16-bit rows of up to 1024: 52 us one after the other, 45 side by side on 52 + 100 SMs (51 on 32 + 120 or 76 + 76);
+// 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 85, and 71 on 32 + 120 (75 on 48 + 104); 256
+// behind 32768: 132, and 121 on 128 + 24 (125 on 132 + 20).
+// The lengths are on the device, so the own rows are taken to be a little over half of
+// max_len: shorter ones end early and leave the rest to the prefix's few SMs.
+// The workspace's size and the launch have to get the same plan: one copy of the arithmetic, never inlined.
+struct ServePlan {
+  PrefixPlan pre;
+  int own_sms;
+  bool together;  // the prefix goes first, and the own rows start on the SMs that it leaves
+};
+__noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_len, int D, int elem_bytes) {
+  ServePlan s;
+  s.together = np > 0 && max_len > 0;
+  s.pre = prefix_plan(B, Hk, gq, np, kSms);
+  s.own_sms = kSms;
+  if (!s.together) return s;
+  // Times in us, fitted to the CTAs of those and other batches.  Own rows on m SMs, two CTAs an SM: 6 to begin, a
+  // tile 1.1 (16 rows 1.3, 24 rows 1.7), a run 3 (16-bit 1, 24 rows 7), and no less than the stream at 6.5 TB/s.
+  const int rows = own_rows(gq);
+  const double units = (double)B * Hk * ((gq + rows - 1) / rows), tiles = units * (0.55 * max_len / kOwnTile + 0.5);
+  const double tile_us = rows <= 8 ? 1.1 : rows == 16 ? 1.3 : 1.7, run_us = rows == 24 ? 7.0 : elem_bytes == 1 ? 3.0 : 1.0;
+  const double stream = 6 + tiles * (2.0 * kOwnTile * D * elem_bytes) / 6.5e6;
+  const double own0 = 6 + run_us, own = (tiles * tile_us + units * run_us) / 2;
+  // The prefix on n SMs: 9 at its ends, a step 1.7 with halved keys, else 1.6, or 2.2 beside a stream that takes the
+  // memory's rate.
+  const double step_us = (s.pre.split ? 1.7 : stream - 6 > own / kSms ? 2.2 : 1.6) * (D == 128 ? 1.0 : 0.65);
+  const double steps = (double)s.pre.units * s.pre.steps, pre = steps * step_us;
+  // own0 + own / (kSms - n) = 9 + pre / n
+  const double d = own0 - 9, b = d * kSms + own + pre;
+  double n = 2 * pre * kSms / (b + sqrt(b * b - 4 * d * pre * kSms));
+  if (own0 + own / (kSms - n) < stream && stream > 9 + pre / n) n = pre / (stream - 9);
+  const int ctas = n < 1 ? 1 : n > kSms - 4 ? kSms - 4 : (int)ceil(n);
+  s.pre = prefix_plan(B, Hk, gq, np, ctas);  // whole steps a CTA: it may take fewer
+  s.own_sms = kSms - s.pre.ctas;
+  return s;
 }
 // The state's place of a unit's part that CTA `cta` works on.
 __device__ __forceinline__ int prefix_part(const PrefixPlan& p, int unit, int cta) {

@@ -707,10 +707,12 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   tc_fence_before();
   __syncthreads();
   if (warp == kOwnMmaWarp) tmem_dealloc(tmem, C::kCols);
+  // this kernel's end has to mean the end of the pass over the prefix too
+  if (threadIdx.x == 0) grid_wait();
 }
 
 template <int Kind, int D, int R>
-cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, cudaStream_t s) {
+cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, int sms, bool after, cudaStream_t s) {
   using C = OwnCfg<Kind, D, R>;
   OwnParams p;
   p.a = a;
@@ -722,23 +724,23 @@ cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, cudaStream_t s) {
     return note_error("cache tensor map encode", cudaErrorInvalidValue);
   const cudaError_t e = cudaFuncSetAttribute(own_kernel<Kind, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return note_error("cached decoding smem attribute", e);
-  return note_error("cached decoding launch", launch_serve_kernel(own_kernel<Kind, D, R>, kOwnCtas / 2 * C::kPerSm,
-                                                                  kOwnThreads, C::kSmem, false, s, p));
+  return note_error("cached decoding launch", launch_serve_kernel(own_kernel<Kind, D, R>, sms * C::kPerSm, kOwnThreads,
+                                                                  C::kSmem, after, s, p));
 }
 
 template <int Kind>
-cudaError_t launch_own_k(const ServeArgs& a, int D, bool q_f16, cudaStream_t s) {
+cudaError_t launch_own_k(const ServeArgs& a, int D, bool q_f16, int sms, bool after, cudaStream_t s) {
   const int r = own_rows(a.group * a.nq);
   if (D == 64) {
-    if (r == 4) return launch_own_r<Kind, 64, 4>(a, q_f16, s);
-    if (r == 8) return launch_own_r<Kind, 64, 8>(a, q_f16, s);
-    if (r == 16) return launch_own_r<Kind, 64, 16>(a, q_f16, s);
-    return launch_own_r<Kind, 64, 24>(a, q_f16, s);
+    if (r == 4) return launch_own_r<Kind, 64, 4>(a, q_f16, sms, after, s);
+    if (r == 8) return launch_own_r<Kind, 64, 8>(a, q_f16, sms, after, s);
+    if (r == 16) return launch_own_r<Kind, 64, 16>(a, q_f16, sms, after, s);
+    return launch_own_r<Kind, 64, 24>(a, q_f16, sms, after, s);
   }
-  if (r == 4) return launch_own_r<Kind, 128, 4>(a, q_f16, s);
-  if (r == 8) return launch_own_r<Kind, 128, 8>(a, q_f16, s);
-  if (r == 16) return launch_own_r<Kind, 128, 16>(a, q_f16, s);
-  return launch_own_r<Kind, 128, 24>(a, q_f16, s);
+  if (r == 4) return launch_own_r<Kind, 128, 4>(a, q_f16, sms, after, s);
+  if (r == 8) return launch_own_r<Kind, 128, 8>(a, q_f16, sms, after, s);
+  if (r == 16) return launch_own_r<Kind, 128, 16>(a, q_f16, sms, after, s);
+  return launch_own_r<Kind, 128, 24>(a, q_f16, sms, after, s);
 }
 
 }  // namespace

@@ -3,8 +3,8 @@
 
 namespace fa {
 
-cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, cudaStream_t s) {
-  return f16 ? launch_own_k<kF16>(a, D, true, s) : launch_own_k<kBf16>(a, D, false, s);
+cudaError_t launch_own_16(const ServeArgs& a, int D, bool f16, int sms, bool after, cudaStream_t s) {
+  return f16 ? launch_own_k<kF16>(a, D, true, sms, after, s) : launch_own_k<kBf16>(a, D, false, sms, after, s);
 }
 
 }  // namespace fa

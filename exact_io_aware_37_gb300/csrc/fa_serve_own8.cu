@@ -3,8 +3,8 @@
 
 namespace fa {
 
-cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, cudaStream_t s) {
-  return launch_own_k<kE4m3>(a, D, q_f16, s);
+cudaError_t launch_own_e4m3(const ServeArgs& a, int D, bool q_f16, int sms, bool after, cudaStream_t s) {
+  return launch_own_k<kE4m3>(a, D, q_f16, sms, after, s);
 }
 
 }  // namespace fa

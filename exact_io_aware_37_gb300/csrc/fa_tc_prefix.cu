@@ -471,12 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-  // this kernel's end has to mean the end of the pass over the own rows too
-  if (threadIdx.x == 0) grid_wait();
 }
 
 template <int D, bool F16, bool kSplit>
-cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, bool after, cudaStream_t s) {
+cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
   using C = Cfg<D>;
   PrefixParams p;
   p.a = a;
@@ -487,19 +485,19 @@ cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, bool aft
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return note_error("prefix smem attribute", e);
   return note_error("prefix launch", launch_serve_kernel(tc_prefix_kernel<D, F16, kSplit>, plan.ctas, kThreads,
-                                                         C::kSmemBytes, after, s, p));
+                                                         C::kSmemBytes, false, s, p));
 }
 
 template <int D, bool F16>
-cudaError_t launch_prefix_f(const ServeArgs& a, const PrefixPlan& plan, bool after, cudaStream_t s) {
-  return plan.split ? launch_prefix_d<D, F16, true>(a, plan, after, s) : launch_prefix_d<D, F16, false>(a, plan, after, s);
+cudaError_t launch_prefix_f(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
+  return plan.split ? launch_prefix_d<D, F16, true>(a, plan, s) : launch_prefix_d<D, F16, false>(a, plan, s);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, bool after, cudaStream_t s) {
-  if (D == 64) return f16 ? launch_prefix_f<64, true>(a, plan, after, s) : launch_prefix_f<64, false>(a, plan, after, s);
-  return f16 ? launch_prefix_f<128, true>(a, plan, after, s) : launch_prefix_f<128, false>(a, plan, after, s);
+cudaError_t launch_prefix(const ServeArgs& a, const PrefixPlan& plan, int D, bool f16, cudaStream_t s) {
+  if (D == 64) return f16 ? launch_prefix_f<64, true>(a, plan, s) : launch_prefix_f<64, false>(a, plan, s);
+  return f16 ? launch_prefix_f<128, true>(a, plan, s) : launch_prefix_f<128, false>(a, plan, s);
 }
 
 }  // namespace fa
