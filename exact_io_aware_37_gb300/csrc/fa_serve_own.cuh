@@ -87,15 +87,17 @@ struct OwnCfg {
   static constexpr int kPRow = kOwnTile * kElem;          // P^T: a row's 128 weights
   static constexpr int kPBlocks = kPRow / 128;
   static constexpr int kPBlock = kN * 128;
-  static constexpr int kPOff = 0;
-  static constexpr int kQOff = (kPBlocks * kPBlock + 1023) / 1024 * 1024;
+  static constexpr int kPBytes = (kPBlocks * kPBlock + 1023) / 1024 * 1024;
+  static constexpr int kPOff = 0;  // two: the next tile is weighed while a product reads this one's
+  static constexpr int kQOff = 2 * kPBytes;
   static constexpr int kRingOff = kQOff + (kBlocks * kQBlock + 1023) / 1024 * 1024;
   // at D = 64 the second half of V^T's 128 rows is read from what follows V (its products go to
   // tensor-memory lanes that nothing reads); past the ring's last slot that is this many bytes
   static constexpr int kPad = D == 64 ? kTileBytes : 0;
-  // as many slots as leave room for a second CTA on the SM, if that is three (a third CTA, at the
-  // same bytes in flight, gained nothing)
-  static constexpr int kFit = (110 * 1024 - kRingOff - kPad) / kTileBytes;
+  // as many slots as leave room for a second CTA on the SM (228 KB; each also takes 1 KB of the
+  // system's, 1 KB for alignment and up to 3 KB below), if that is three (a third CTA, at the same
+  // bytes in flight, gained nothing)
+  static constexpr int kFit = (108 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kSlots = kFit >= 3 ? (kFit < 8 ? kFit : 8) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
   static constexpr int kSmem = kRingOff + kSlots * kTileBytes + kPad + 1024;
@@ -173,11 +175,12 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // Steps (tiles) g are counted over all of a CTA's runs.  full / free: the ring; bar_s[g % 2]:
-  // S^T(g) complete; bar_p: P^T(g) written and S^T(g) read out (the MMA thread has waited for
-  // it before it issues S^T(g + 2) over the same columns); bar_o: O^T += (g) complete; bar_q: a
-  // run's Q written.
+  // S^T(g) complete; bar_p[g % 2]: P^T(g) written and S^T(g) read out (the MMA thread has waited
+  // for it before it issues S^T(g + 2) over the same columns); bar_o[g % 2]: O^T += (g) complete (S^T(g)
+  // is issued behind O^T += (g - 2), so with bar_s P^T(g)'s place is free, and bar_o's phase before this
+  // one over); bar_q: a run's Q written.
   __shared__ __align__(8) uint64_t bar_full[H], bar_free[H];
-  __shared__ __align__(8) uint64_t bar_s[2], bar_p, bar_o, bar_q, bar_done;
+  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2], bar_o[2], bar_q, bar_done;
   // by the run's parity: the next run's are written while this one's are in use
   __shared__ __align__(16) RowInfo s_row[2][R];
   __shared__ float s_refw[2][R], s_refl[2][R];  // references of the weights and of the normaliser
@@ -198,9 +201,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_free[s], 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&bar_s[s], 1);
-    mbar_init(&bar_p, 4);
-    mbar_init(&bar_o, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar_s[s], 1);
+      mbar_init(&bar_p[s], 4);
+      mbar_init(&bar_o[s], 1);
+    }
     mbar_init(&bar_q, 4);
     mbar_init(&bar_done, 1);
     abort_flag = 0;
@@ -262,7 +267,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     const int tid = threadIdx.x;  // the key of a tile that this thread holds
     const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t t_o = t_s + 2 * C::kN;
-    uint8_t* sp = smem + C::kPOff;
     uint8_t* sq = smem + C::kQOff;
     constexpr int kRowThreads = D / 8;  // threads of a query row, 8 elements each
     constexpr int kPass = 128 / kRowThreads, kPasses = (R + kPass - 1) / kPass;
@@ -395,6 +399,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         ok = ok && warp_wait(&bar_s[g & 1], (g >> 1) & 1, w);
         tc_fence_after();
         const uint32_t at_s = t_s + (g & 1) * C::kN;
+        uint8_t* sp = smem + C::kPOff + (g & 1) * C::kPBytes;
         const bool edge = key0 + kOwnTile > lim_all;
         // At the edge: values of keys past the end become zero, and so do those that are
         // not finite of keys that only some rows see (0 * NaN would reach the rows that
@@ -528,11 +533,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           }
           weigh_tile(Flag<true>{});
         } else {
-          // P^T's place is free, and O^T at rest, once the step before has been added
-          ok = ok && warp_wait(&bar_o, (g - 1) & 1, w);
-          tc_fence_after();
           const bool over = weigh_tile(Flag<true>{});
           if (named_bar_or(1, 128, over || !ok)) {
+            // O^T is at rest once the last step has been added
+            ok = ok && warp_wait(&bar_o[(g - 1) & 1], ((g - 1) >> 1) & 1, w);
+            tc_fence_after();
             if (!refer()) {
               ok = false;
               break;
@@ -558,13 +563,13 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p);
+        if (lane == 0) mbar_arrive(&bar_p[g & 1]);
       }
       // ---- the next run's queries, while this one's last product runs
       const unsigned last = g - 1;
       if (!named_bar_and(1, 128, ok)) break;
       if (have) put_q(nx, par ^ 1);
-      ok = named_bar_and(1, 128, warp_wait(&bar_o, last & 1, w));
+      ok = named_bar_and(1, 128, warp_wait(&bar_o[last & 1], (last >> 1) & 1, w));
       if (!ok) break;
       tc_fence_after();
 
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     const uint64_t dk0 = desc(smem + C::kRingOff, 16);
     const uint64_t dv0 = desc(smem + C::kRingOff, C::kBlockBytes);  // V^T: MN-major, the next elements a block further
     const uint64_t dq0 = desc(smem + C::kQOff, 16);
-    const uint64_t dp0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);
+    const uint64_t dp0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);  // of even steps
     bool ok = true;
     unsigned g = 0;
     int run = 0;
@@ -662,17 +667,17 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     // O^T += V^T P^T of step x
     auto add = [&](unsigned x, bool acc) -> bool {
       const unsigned h = 2 * x + 1, s = h % H;
-      if (!mbar_wait(&bar_full[s], (h / H) & 1, w) || !mbar_wait(&bar_p, x & 1, w)) return false;
+      if (!mbar_wait(&bar_full[s], (h / H) & 1, w) || !mbar_wait(&bar_p[x & 1], (x >> 1) & 1, w)) return false;
       tc_fence_after();
-      const uint64_t v = dv0 + ((s * C::kTileBytes) >> 4);
+      const uint64_t v = dv0 + ((s * C::kTileBytes) >> 4), pt = dp0 + (((x & 1) * C::kPBytes) >> 4);
 #pragma unroll
       for (int k = 0; k < kOwnTile / kStep; ++k) {
         const int byte = k * 32;  // of a row of P^T
-        mma(tmem + 2 * C::kN, v + ((k * kStep * C::kPitch) >> 4), dp0 + (((byte >> 7) * C::kPBlock + (byte & 127)) >> 4),
+        mma(tmem + 2 * C::kN, v + ((k * kStep * C::kPitch) >> 4), pt + (((byte >> 7) * C::kPBlock + (byte & 127)) >> 4),
             id_o, acc || k > 0);
       }
       mma_commit(&bar_free[s]);
-      mma_commit(&bar_o);
+      mma_commit(&bar_o[x & 1]);
       return true;
     };
     bool have = next_run(walk, q);

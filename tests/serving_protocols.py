@@ -102,9 +102,11 @@ def run_own(runs, seed, H=3, W=3, skip=()):
     m = Machine(rng)
     full, free = [Bar(f"full{i}", 1) for i in range(H)], [Bar(f"free{i}", 1) for i in range(H)]
     s = [Bar(f"s{i}", 1) for i in range(2)]
-    p, o, q = Bar("p", W), Bar("o", 1), Bar("q", W)
+    p, o, q = [Bar(f"p{i}", W) for i in range(2)], [Bar(f"o{i}", 1) for i in range(2)], Bar("q", W)
     meet = Rendezvous(W)
-    state = {"o": 0, "read": 0}  # runs whose first P V overwrote O^T; runs read out by every warp
+    # runs whose first P V overwrote O^T; runs read out by every warp; steps added
+    state = {"o": 0, "read": 0, "added": 0}
+    outgrown = [rng.random() < 0.4 for _ in range(sum(runs))]  # steps that are weighed again
 
     def maybe(name, gen):
         if name not in skip:
@@ -127,16 +129,17 @@ def run_own(runs, seed, H=3, W=3, skip=()):
         def add(x, run, acc):
             h = 2 * x + 1
             yield from wait(full[h % H], h // H)
-            yield from maybe("p", wait(p, x))
+            yield from maybe("p", wait(p[x & 1], x >> 1))
 
             def effect():
+                state["added"] += 1
                 if not acc:
                     assert state["read"] == run * W, "O^T overwritten before it was read out"
                     state["o"] = run + 1
 
-            m.product({("ring", h % H): h, **{("P", w): x for w in range(W)}}, effect)
+            m.product({("ring", h % H): h, **{("P", x & 1, w): x for w in range(W)}}, effect)
             m.commit(free[h % H])
-            m.commit(o)
+            m.commit(o[x & 1])
 
         for run, n in enumerate(runs):
             yield from maybe("q", wait(q, run))
@@ -173,20 +176,23 @@ def run_own(runs, seed, H=3, W=3, skip=()):
                 if i == 0:  # references, then the weights
                     yield from meet.come()
                     yield from meet.come()
-                else:
-                    yield from maybe("o", wait(o, g - 1))
-                for again in range(1 + (i > 0)):
+                for again in range(1 + (i > 0 and outgrown[g])):
                     assert m.has.get(("S", g & 1, w)) == g, "scores overwritten while in use"
-                    m.write(("P", w), g)
+                    m.write(("P", g & 1, w), g)
                     yield
                     if i > 0 and not again:
-                        yield from meet.come()  # the vote; then perhaps once more
-                p.arrive()
+                        yield from meet.come()  # the vote
+                        if outgrown[g]:  # references, O^T rescaled, and once more
+                            yield from maybe("o", wait(o[(g - 1) & 1], (g - 1) >> 1))
+                            yield from meet.come()
+                            yield from meet.come()
+                            assert state["added"] == g, "O^T rescaled while steps are missing"
+                p[g & 1].arrive()
                 g += 1
             yield from meet.come()
             if run + 1 < len(runs):
                 yield from put_q(run + 1)
-            yield from maybe("o_end", wait(o, g - 1))
+            yield from maybe("o_end", wait(o[(g - 1) & 1], (g - 1) >> 1))
             yield from meet.come()
             assert state["o"] == run + 1, "state read before the run's products"
             state["read"] += 1
