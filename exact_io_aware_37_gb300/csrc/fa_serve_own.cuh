@@ -84,10 +84,12 @@ struct OwnCfg {
   static constexpr int kTerms = kCodes ? 3 : 1;
   static constexpr int kN = (R * kTerms + 15) / 16 * 16;  // columns of the narrow operand; term x of row r is x R + r
   static constexpr int kQBlock = kN * kPitch;             // Q: the same blocks, kN rows
-  static constexpr int kPRow = kOwnTile * kElem;          // P^T: a row's 128 weights
-  static constexpr int kPBlocks = kPRow / 128;
-  static constexpr int kPBlock = kN * 128;
-  static constexpr int kPBytes = (kPBlocks * kPBlock + 1023) / 1024 * 1024;
+  // P^T.  Codes: a key's weights together, 32 columns of all keys a block (MN-major, 32-byte swizzle), so that a
+  // thread stores eight rows' bytes of a term at once (a byte a row and term, K-major: 94 us a step where this
+  // takes 88, 24 sequences of up to 16384 keys, 20 query rows a key head).  16-bit: a row's 128 weights together, in two blocks.
+  static constexpr int kPN = kCodes ? (kN + 31) / 32 * 32 : kN;  // columns of the second product
+  static constexpr int kPBlock = kCodes ? kOwnTile * 32 : kN * 128;
+  static constexpr int kPBytes = ((kCodes ? kPN / 32 : 2) * kPBlock + 1023) / 1024 * 1024;
   static constexpr int kPOff = 0;  // two: the next tile is weighed while a product reads this one's
   static constexpr int kQOff = 2 * kPBytes;
   static constexpr int kRingOff = kQOff + (kBlocks * kQBlock + 1023) / 1024 * 1024;
@@ -101,7 +103,7 @@ struct OwnCfg {
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kSlots = kFit >= 3 ? (kFit < 8 ? kFit : 8) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
   static constexpr int kSmem = kRingOff + kSlots * kTileBytes + kPad + 1024;
-  static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;  // two S^T, O^T
+  static constexpr int kCols = 2 * kN + kPN <= 64 ? 64 : 2 * kN + kPN <= 128 ? 128 : 256;  // two S^T, O^T
   static constexpr int kChunk = R < 8 ? R : 8;                                 // rows read out together
 };
 
@@ -501,18 +503,22 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
               else
                 t[e / 2][0] = pack16x2<Kind == kF16>(v[e], v[e + 1]);
             }
+            if constexpr (C::kCodes) {
 #pragma unroll
-            for (int e = 0; e < C::kChunk; e += 2) {
-              const int r = r0 + e;
-              if (r >= valid) break;
-              if constexpr (C::kCodes) {
+              for (int k = 0; k < 3; ++k) {
+                const int col = k * R + r0;
+                uint8_t* dst = sp + col / 32 * C::kPBlock + tid * 32 + ((col >> 4 ^ tid >> 2) & 1) * 16 + (col & 15);
+                if constexpr (C::kChunk == 8)
+                  *reinterpret_cast<uint2*>(dst) =
+                      make_uint2(__byte_perm(t[0][k], t[1][k], 0x5410), __byte_perm(t[2][k], t[3][k], 0x5410));
+                else
+                  *reinterpret_cast<uint32_t*>(dst) = __byte_perm(t[0][k], t[1][k], 0x5410);
+              }
+            } else {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                  const int at = k * R + r;
-                  sp[swz<128>(at, tid >> 4) + (tid & 15)] = (uint8_t)t[e / 2][k];
-                  sp[swz<128>(at + 1, tid >> 4) + (tid & 15)] = (uint8_t)(t[e / 2][k] >> 8);
-                }
-              } else {
+              for (int e = 0; e < C::kChunk; e += 2) {
+                const int r = r0 + e;
+                if (r >= valid) break;
                 uint8_t* dst = sp + (tid >> 6) * C::kPBlock + (tid & 7) * 2;
                 *reinterpret_cast<uint16_t*>(dst + swz<128>(r, (tid & 63) >> 3)) = (uint16_t)t[e / 2][0];
                 *reinterpret_cast<uint16_t*>(dst + swz<128>(r + 1, (tid & 63) >> 3)) = (uint16_t)(t[e / 2][0] >> 16);
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     // ------------------------------------------------------------ MMA issuer
     constexpr int kStep = C::kCodes ? 32 : 16;  // elements of one MMA's reduction
     constexpr uint32_t id_s = C::kCodes ? idesc_e4m3(128, C::kN, false, false) : idesc16<Kind == kF16>(128, C::kN, false, false);
-    constexpr uint32_t id_o = C::kCodes ? idesc_e4m3(128, C::kN, true, false) : idesc16<Kind == kF16>(128, C::kN, true, false);
+    constexpr uint32_t id_o = C::kCodes ? idesc_e4m3(128, C::kPN, true, true) : idesc16<Kind == kF16>(128, C::kN, true, false);
     auto desc = [](const uint8_t* at, uint32_t lbo) {
       return C::kPitch == 128 ? sdesc_sw128(smem_u32(at), lbo, 1024) : sdesc_sw64(smem_u32(at), lbo, 512);
     };
@@ -659,7 +665,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     const uint64_t dk0 = desc(smem + C::kRingOff, 16);
     const uint64_t dv0 = desc(smem + C::kRingOff, C::kBlockBytes);  // V^T: MN-major, the next elements a block further
     const uint64_t dq0 = desc(smem + C::kQOff, 16);
-    const uint64_t dp0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);  // of even steps
+    const uint64_t dp0 = C::kCodes ? sdesc_sw32(smem_u32(smem + C::kPOff), C::kPBlock, 256)
+                                   : sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);  // of even steps
     bool ok = true;
     unsigned g = 0;
     int run = 0;
@@ -672,8 +679,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
       const uint64_t v = dv0 + ((s * C::kTileBytes) >> 4), pt = dp0 + (((x & 1) * C::kPBytes) >> 4);
 #pragma unroll
       for (int k = 0; k < kOwnTile / kStep; ++k) {
-        const int byte = k * 32;  // of a row of P^T
-        mma(tmem + 2 * C::kN, v + ((k * kStep * C::kPitch) >> 4), pt + (((byte >> 7) * C::kPBlock + (byte & 127)) >> 4),
+        // codes: 32 keys of 32 bytes on; 16-bit: 32 bytes of a row
+        const int on = C::kCodes ? k * 1024 : (k >> 2) * C::kPBlock + (k & 3) * 32;
+        mma(tmem + 2 * C::kN, v + ((k * kStep * C::kPitch) >> 4), pt + (on >> 4),
             id_o, acc || k > 0);
       }
       mma_commit(&bar_free[s]);
