@@ -85,8 +85,8 @@ struct OwnCfg {
   static constexpr int kN = (R * kTerms + 15) / 16 * 16;  // columns of the narrow operand; term x of row r is x R + r
   static constexpr int kQBlock = kN * kPitch;             // Q: the same blocks, kN rows
   // P^T.  Codes: a key's weights together, 32 columns of all keys a block (MN-major, 32-byte swizzle), so that a
-  // thread stores eight rows' bytes of a term at once (a byte a row and term, K-major: 94 us a step where this
-  // takes 88, 24 sequences of up to 16384 keys, 20 query rows a key head).  16-bit: a row's 128 weights together, in two blocks.
+  // thread stores eight rows' bytes of a term at once (a byte a row and term, K-major: 94 us a step, so
+  // 88, 24 sequences of up to 16384 keys, 20 query rows a key head).  16-bit: a row's 128 weights together, in two blocks.
   static constexpr int kPN = kCodes ? (kN + 31) / 32 * 32 : kN;  // columns of the second product
   static constexpr int kPBlock = kCodes ? kOwnTile * 32 : kN * 128;
   static constexpr int kPBytes = ((kCodes ? kPN / 32 : 2) * kPBlock + 1023) / 1024 * 1024;
@@ -158,11 +158,12 @@ __device__ __forceinline__ void sum_rows(float (&l)[R], int lane) {
   for (int m = R2; m < 32; m <<= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], m);
 }
 
-// What the threads share about a query row of a run.
-struct RowInfo {
-  float factor;        // from products to log2 units
-  float neg_w, neg_l;  // minus the references (neg_w holds the weights' scale)
-  int limit;           // keys it sees
+// What the threads share about two query rows of a run (x and y; two, for the packed float32 arithmetic).
+struct RowPair {
+  float2 factor;  // from products to log2 units
+  float2 neg_w;   // minus the references (neg_w holds the weights' scale)
+  float2 neg_l;
+  int2 limit;     // keys they see
 };
 // In place of minus a reference while a row has seen no score above -inf: any such score
 // outgrows it.
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
   __shared__ __align__(8) uint64_t bar_full[H], bar_free[H];
   __shared__ __align__(8) uint64_t bar_s[2], bar_p[2], bar_o[2], bar_q, bar_done;
   // by the run's parity: the next run's are written while this one's are in use
-  __shared__ __align__(16) RowInfo s_row[2][R];
+  __shared__ __align__(16) RowPair s_row[2][R / 2];
   __shared__ float s_refw[2][R], s_refl[2][R];  // references of the weights and of the normaliser
   __shared__ float s_mw[4][R], s_ml[4][R];      // warps' maxima
   __shared__ float s_sum[4][R];                 // and sums, at a run's end
@@ -274,6 +275,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     constexpr int kPass = 128 / kRowThreads, kPasses = (R + kPass - 1) / kPass;
     const int qr = tid / kRowThreads, qx = tid % kRowThreads * 8;
 
+    auto row_of = [&](auto field, int par, int r) -> auto& {
+      auto& two = s_row[par][r >> 1].*field;
+      return r & 1 ? two.y : two.x;
+    };
     // ---- a run's queries: loaded early, put in place later
     uint4 qv[kPasses];
     auto load_q = [&](const Run& q) {
@@ -331,7 +336,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           // a row past the last weighs nothing and outgrows nothing
           const bool there = r < valid;
           const int limit = a.causal ? max(0, q.len - a.nq + (q.row0 + r) % a.nq + 1) : q.len;
-          s_row[par][r] = RowInfo{factor, there ? kNoReference : -INFINITY, there ? kNoReference : -INFINITY, limit};
+          row_of(&RowPair::factor, par, r) = factor;
+          row_of(&RowPair::neg_w, par, r) = row_of(&RowPair::neg_l, par, r) = there ? kNoReference : -INFINITY;
+          row_of(&RowPair::limit, par, r) = limit;
           s_refw[par][r] = s_refl[par][r] = there ? -INFINITY : INFINITY;
         }
       }
@@ -358,10 +365,15 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 #pragma unroll
       for (int k = 0; k < C::kTerms; ++k) tmem_ld_wait(x[k]);
 #pragma unroll
-      for (int e = 0; e < C::kChunk; ++e) {
-        v[e] = __uint_as_float(x[0][e]);
-        if constexpr (C::kCodes)
-          v[e] = fmaf(fmaf(__uint_as_float(x[2][e]), c8::kTerm, __uint_as_float(x[1][e])), c8::kTerm, v[e]);
+      for (int e = 0; e < C::kChunk; e += 2) {
+        auto as = [&](int k, int i) { return __uint_as_float(x[k][e + i]); };
+        v[e] = as(0, 0);
+        v[e + 1] = as(0, 1);
+        if constexpr (C::kCodes) {
+          float lo, hi;
+          ffma2(lo, hi, as(2, 0), as(2, 1), c8::kTerm, as(1, 0), as(1, 1));
+          ffma2(v[e], v[e + 1], lo, hi, c8::kTerm, v[e], v[e + 1]);
+        }
       }
     };
 
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
     while (ok && have) {
       const int valid = min(R, rows - q.row0);
       const int lim_all = a.causal ? max(0, q.len - a.nq + 1) : q.len;  // keys that every row sees
-      const RowInfo* row = s_row[par];
+      const RowPair* row = s_row[par];
       float l[R];  // this thread's share of the normaliser
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.f;
@@ -436,8 +448,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             read_chunk(at_s + r0, v);
 #pragma unroll
             for (int e = 0; e < C::kChunk; ++e) {
-              float x = v[e] * (row[r0 + e].factor * kf);
-              if (edge && key >= row[r0 + e].limit) x = -INFINITY;
+              float x = v[e] * (row_of(&RowPair::factor, par, r0 + e) * kf);
+              if (edge && key >= row_of(&RowPair::limit, par, r0 + e)) x = -INFINITY;
               const float mw = warp_max(x + ve), ml = C::kCodes ? warp_max(x) : mw;
               if (lane == 0) {
                 s_mw[warp][r0 + e] = mw;
@@ -456,8 +468,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             s_fw[tid] = grow(s_refw[par][tid], s_mw[0][tid], s_mw[1][tid], s_mw[2][tid], s_mw[3][tid]);
             s_fl[tid] = grow(s_refl[par][tid], s_ml[0][tid], s_ml[1][tid], s_ml[2][tid], s_ml[3][tid]);
             const float rw = s_refw[par][tid], rl = s_refl[par][tid];
-            s_row[par][tid].neg_w = rw == -INFINITY ? kNoReference : kWeightScale - rw;
-            s_row[par][tid].neg_l = rl == -INFINITY ? kNoReference : -rl;
+            row_of(&RowPair::neg_w, par, tid) = rw == -INFINITY ? kNoReference : kWeightScale - rw;
+            row_of(&RowPair::neg_l, par, tid) = rl == -INFINITY ? kNoReference : -rl;
           }
           named_bar_sync(1, 128);
           return true;
@@ -471,30 +483,44 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 #pragma unroll
           for (int r0 = 0; r0 < R; r0 += C::kChunk) {
             if (r0 >= valid) break;
-            // The chunk's weights first, its stores last: a store of bytes may alias what the next
-            // row would read, and the rows' chains of conversions would run one after another.
             float v[C::kChunk];
             uint32_t t[C::kChunk / 2][C::kTerms];
             read_chunk(at_s + r0, v);
 #pragma unroll
-            for (int e = 0; e < C::kChunk; ++e) {
-              const RowInfo info = row[r0 + e];
-              const float f = info.factor * kf;
-              const bool hidden = at_edge.value && key >= info.limit;
-              const float x = hidden ? -INFINITY : fmaf(v[e], f, info.neg_w + ve);
-              float sum = 0.f;
+            for (int e = 0; e < C::kChunk; e += 2) {
+              const RowPair two = row[(r0 + e) / 2];
+              const bool hide0 = at_edge.value && key >= two.limit.x, hide1 = at_edge.value && key >= two.limit.y;
+              float2 f = two.factor, nw = two.neg_w;
               if constexpr (C::kCodes) {
-                const float y = hidden ? -INFINITY : fmaf(v[e], f, info.neg_l);
-                sum = ex2_approx(y);
-                if (first.value) most_l = fmaxf(most_l, y);
+                fmul2(f.x, f.y, f.x, f.y, kf, kf);
+                fadd2(nw.x, nw.y, ve, ve);
               }
-              if (first.value) most_w = fmaxf(most_w, x);
-              v[e] = ex2_approx(x);
-              if constexpr (!C::kCodes) sum = v[e];
-              if (first.value)
-                l[r0 + e] += sum;
-              else if (l[r0 + e] == INFINITY)
-                l[r0 + e] = sum;
+              float x0, x1, sum0, sum1;
+              ffma2(x0, x1, v[e], v[e + 1], f, nw);
+              if (hide0) x0 = -INFINITY;
+              if (hide1) x1 = -INFINITY;
+              if constexpr (C::kCodes) {
+                float y0, y1;
+                ffma2(y0, y1, v[e], v[e + 1], f, two.neg_l);
+                if (hide0) y0 = -INFINITY;
+                if (hide1) y1 = -INFINITY;
+                sum0 = ex2_approx(y0);
+                sum1 = ex2_approx(y1);
+                if (first.value) most_l = fmaxf(most_l, fmaxf(y0, y1));
+              }
+              if (first.value) most_w = fmaxf(most_w, fmaxf(x0, x1));
+              v[e] = ex2_approx(x0);
+              v[e + 1] = ex2_approx(x1);
+              if constexpr (!C::kCodes) {
+                sum0 = v[e];
+                sum1 = v[e + 1];
+              }
+              if (first.value) {
+                fadd2(l[r0 + e], l[r0 + e + 1], sum0, sum1);
+              } else {
+                if (l[r0 + e] == INFINITY) l[r0 + e] = sum0;
+                if (l[r0 + e + 1] == INFINITY) l[r0 + e + 1] = sum1;
+              }
             }
 #pragma unroll
             for (int e = 0; e < C::kChunk; e += 2) {
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             float u = C::kCodes ? v[e] * (1.f / (1 << (int)kWeightLog2)) : v[e];
             if (bad) {  // what is not finite of keys that not all rows see
               const int k0 = max(lim_all, q.tile0 * kOwnTile);
-              const int k1 = min(row[r].limit, (q.tile0 + q.n) * kOwnTile);
+              const int k1 = min(row_of(&RowPair::limit, par, r), (q.tile0 + q.n) * kOwnTile);
               for (int key = k0; key < k1; ++key) {
                 const float y = cache_value<Kind>(static_cast<const uint8_t*>(a.v) +
                                                   (((long long)q.slab * a.cap + key) * D + tid) * C::kElem);

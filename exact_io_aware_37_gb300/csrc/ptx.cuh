@@ -512,6 +512,13 @@ __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, 
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1)
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float2 b, float2 c) {
+  asm("{\n .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+      " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+}
 // (s0, s1) += (a0, a1)
 __device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) {
   asm("{\n .reg .b64 ra, rs;\n mov.b64 ra, {%2, %3};\n mov.b64 rs, {%0, %1};\n add.rn.f32x2 rs, rs, ra;\n"
