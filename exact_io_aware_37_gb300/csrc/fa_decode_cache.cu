@@ -257,9 +257,9 @@ size_t serve_workspace_bytes(int B, int H, int Hk, int nq, int np, int max_len, 
 
 cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cudaStream_t s) {
   const bool f16 = dt == FA_F16;
-  a.run_cost = own_run_cost(a.k_exp ? 1 : 2, D);
   MergeParams m;
   m.cta_rows = own_rows(a.group * a.nq);
+  a.run_cost = own_run_cost(m.cta_rows, a.k_exp ? 1 : 2, D);
   m.row_groups = (a.group * a.nq + m.cta_rows - 1) / m.cta_rows;
   const ServePlan plan = serve_plan(a.B, a.Hk, a.group * a.nq, a.np, a.max_len, D, a.k_exp ? 1 : 2);
   m.pre = plan.pre;

@@ -18,10 +18,12 @@ constexpr int kSms = 152;
 constexpr int kOwnCtas = 2 * kSms;
 constexpr int kOwnTile = 128;  // keys of a step
 // What a run costs besides its tiles (queries in, references found, state out), in tiles: it
-// only steers the cut.  About as long as 96 KB of cache take: fitted over the CTAs of
-// ragged batches, 3 tiles of 32 KB (8-bit, D = 128, up to 16 rows; 5 at 24 rows), below
-// one of 64 KB (16-bit).  Without it the CTAs that got the short sequences took twice the average.
-inline int own_run_cost(int elem_bytes, int D) { return (96 * 1024) / (2 * kOwnTile * D * elem_bytes); }
+// only steers the cut.  About as long as 96 KB of cache take, 160 KB at 24 rows: fitted over the CTAs of
+// ragged batches, 3 and 5 tiles of 32 KB (8-bit, D = 128), below one of 64 KB (16-bit).  Without it the CTAs that got
+// the short sequences took twice the average; 24 rows of 24 sequences of up to 16384 keys took 88 us with 3, 84 with 5.
+inline int own_run_cost(int cta_rows, int elem_bytes, int D) {
+  return (cta_rows == 24 ? 160 : 96) * 1024 / (2 * kOwnTile * D * elem_bytes);
+}
 // Query rows of a CTA: what the rows of a key head fill, so that fewer rows leave fewer
 // columns to multiply and read out.  More than 24 are spread over row groups, which
 // read the same keys at about the same time, so mostly from L2.
@@ -179,10 +181,10 @@ __noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_
   s.own_sms = kSms;
   if (!s.together) return s;
   // Times in us, fitted to the CTAs of those and other batches.  Own rows on m SMs, two CTAs an SM: 6 to begin, a
-  // tile 1.1 (16 rows 1.3, 24 rows 1.7), a run 3 (16-bit 1, 24 rows 7), and no less than the stream at 6.5 TB/s.
+  // tile 1.1 (16 rows 1.2, 24 rows 1.5), a run 3 (16-bit 1, 24 rows 5), and no less than the stream at 6.5 TB/s.
   const int rows = own_rows(gq);
   const double units = (double)B * Hk * ((gq + rows - 1) / rows), tiles = units * (0.55 * max_len / kOwnTile + 0.5);
-  const double tile_us = rows <= 8 ? 1.1 : rows == 16 ? 1.3 : 1.7, run_us = rows == 24 ? 7.0 : elem_bytes == 1 ? 3.0 : 1.0;
+  const double tile_us = rows <= 8 ? 1.1 : rows == 16 ? 1.2 : 1.5, run_us = rows == 24 ? 5.0 : elem_bytes == 1 ? 3.0 : 1.0;
   const double stream = 6 + tiles * (2.0 * kOwnTile * D * elem_bytes) / 6.5e6;
   const double own0 = 6 + run_us, own = (tiles * tile_us + units * run_us) / 2;
   // The prefix on n SMs: 9 at its ends, a step 1.7 with halved keys, else 1.6, or 2.2 beside a stream that takes the

@@ -98,10 +98,12 @@ struct OwnCfg {
   static constexpr int kPad = D == 64 ? kTileBytes : 0;
   // as many slots as leave room for a second CTA on the SM (228 KB; each also takes 1 KB of the
   // system's, 1 KB for alignment and up to 3 KB below), if that is three (a third CTA, at the same
-  // bytes in flight, gained nothing)
+  // bytes in flight, gained nothing).  No more than 80 KB: with six slots of 16 KB B16 H32 8192 keys took 159 us
+  // where five take 156 and four 159.5.
   static constexpr int kFit = (108 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
-  static constexpr int kSlots = kFit >= 3 ? (kFit < 8 ? kFit : 8) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
+  static constexpr int kMost = kTileBytes <= 8192 ? 8 : 5;
+  static constexpr int kSlots = kFit >= 3 ? (kFit < kMost ? kFit : kMost) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
   static constexpr int kSmem = kRingOff + kSlots * kTileBytes + kPad + 1024;
   static constexpr int kCols = 2 * kN + kPN <= 64 ? 64 : 2 * kN + kPN <= 128 ? 128 : 256;  // two S^T, O^T
   static constexpr int kChunk = R < 8 ? R : 8;                                 // rows read out together
