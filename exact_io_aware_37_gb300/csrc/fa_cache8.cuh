@@ -38,16 +38,10 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // Two values of magnitude at most 448, or NaN, to two codes (round to nearest
 // even), `lo` in the low byte.
-__device__ __forceinline__ uint32_t encode2_finite(float lo, float hi) {
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
-}
-// The same with infinities, which the conversion would saturate, to NaN.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-  lo = fabsf(lo) < INFINITY ? lo : __uint_as_float(0x7fffffffu);
-  hi = fabsf(hi) < INFINITY ? hi : __uint_as_float(0x7fffffffu);
-  return encode2_finite(lo, hi);
 }
 
 // Two codes (low 16 bits of u) to an fp16 pair, exactly.
