@@ -12,6 +12,7 @@
 // in front of it drains.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fa_internal.cuh"
@@ -23,8 +24,8 @@ namespace {
 
 // Joins the states of every query row: D / 8 lanes a row, eight columns each, one
 // whole sector of a state's row.  The join waits for L2 more than it moves bytes, so
-// where few rows have many states kGroups groups of lanes share a row's (2048 rows of 17 states:
-// four groups 51 us a step, one 66; 3840 rows of 2: 112 and 107; 8192 rows of 7: 139 and 135).
+// where few rows have many states kGroups groups of lanes share a row's (2048 rows of 7 states:
+// four groups 45 us a step, one 50; 3840 rows of 2: 87 and 81; 8192 rows of 5: 132 and 121).
 constexpr int kMergeThreads = 256;
 constexpr long long kFewRows = 4096;
 constexpr int kManyStates = 6;
@@ -200,7 +201,8 @@ cudaError_t launch_merge(const MergeParams& p, int D, cudaStream_t s) {
   const long long rows = (long long)p.a.B * p.a.Hk * p.a.group * p.a.nq;
   // states of a row, about: the prefix's parts, and the CTAs that share a unit of the own rows
   const long long units = (long long)p.a.B * p.a.Hk * p.row_groups;
-  const long long states = (p.a.np > 0 ? (p.pre.steps / p.pre.per_cta + 1) * (p.pre.split ? 2 : 1) : 0) + kOwnCtas / units;
+  const long long states = (p.a.np > 0 ? (p.pre.steps / p.pre.per_cta + 1) * (p.pre.split ? 2 : 1) : 0) +
+                           std::min<long long>(kOwnCtas / units, own_tiles(p.a.max_len));
   const bool few = rows <= kFewRows && states >= kManyStates;
   const int per = kMergeThreads / (D / 8) / (few ? 4 : 1);
   auto* kernel = few ? (D == 64 ? merge_kernel<T, 64, 4> : merge_kernel<T, 128, 4>)
