@@ -39,7 +39,7 @@ __device__ __forceinline__ int seq_len(const ServeArgs& a, int b) {
   const int len = raw_len(a, b);
   return len_ok(a, len) ? len : 0;
 }
-__device__ __forceinline__ int own_tiles(int len) { return (int)(((unsigned)len + kOwnTile - 1) / kOwnTile); }
+__host__ __device__ __forceinline__ int own_tiles(int len) { return (int)(((unsigned)len + kOwnTile - 1) / kOwnTile); }
 // Cost of a unit of `tiles` tiles: the run's own cost, then a tile each.
 __device__ __forceinline__ int own_cost(const ServeArgs& a, int tiles) { return tiles > 0 ? tiles + a.run_cost : 0; }
 
