@@ -164,7 +164,7 @@ inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
 // side by side, the prefix on as many SMs as let both end at about the same time: each pass's
 // start and end (its queries, first copies, states) hides behind the other's stream.  64 sequences behind 8192 keys,
 // 16-bit rows of up to 1024: 52 us one after the other, 45 side by side on 52 + 100 SMs (51 on 32 + 120 or 76 + 76);
-// 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 85, and 71 on 32 + 120 (75 on 48 + 104); 256
+// 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 85, and 70 on 32 + 120 (73 on 43 + 109); 256
 // behind 32768: 132, and 121 on 128 + 24 (125 on 132 + 20).
 // The lengths are on the device, so the own rows are taken to be a little over half of
 // max_len: shorter ones end early and leave the rest to the prefix's few SMs.
@@ -195,8 +195,18 @@ __noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_
   const double d = own0 - 9, b = d * kSms + own + pre;
   double n = 2 * pre * kSms / (b + sqrt(b * b - 4 * d * pre * kSms));
   if (own0 + own / (kSms - n) < stream && stream > 9 + pre / n) n = pre / (stream - 9);
-  const int ctas = n < 1 ? 1 : n > kSms - 4 ? kSms - 4 : (int)ceil(n);
-  s.pre = prefix_plan(B, Hk, gq, np, ctas);  // whole steps a CTA: it may take fewer
+  // The CTAs take whole steps: of the two whole n beside it the one whose longer pass is the shorter (5 sequences of 8 new
+  // tokens, 30 key heads, 28414 + up to 183 keys: 100 us on 148 + 4 SMs, 89 on 145 + 7).
+  double best = 0;
+  for (int i = 0; i < 2; ++i) {
+    const double x = floor(n) + i;
+    const PrefixPlan plan = prefix_plan(B, Hk, gq, np, x < 1 ? 1 : x > kSms - 4 ? kSms - 4 : (int)x);
+    const double own_us = fmax(own0 + own / (kSms - plan.ctas), stream), us = fmax(own_us, 9 + plan.per_cta * step_us);
+    if (i == 0 || us < best) {
+      best = us;
+      s.pre = plan;
+    }
+  }
   s.own_sms = kSms - s.pre.ctas;
   return s;
 }
