@@ -18,15 +18,17 @@
 // normaliser sums the unrounded 2^(s - ref_l).
 //
 // Bound.  Every cache row is read once: HBM.  Per 128 keys of D = 128 codes the
-// tensor core spends 256 cycles, the copies at the full rate 1400.  (The products
+// tensor core spends 256 cycles, the copies at the full rate 1400: B16 H32 8192 keys D128 take 158 us a step (6.8
+// TB/s).  From some 8 query rows a key head on the softmax warps' instructions show: 24 sequences of up to 16384
+// keys, 8 key heads, floor 60 us, take 62 at 4 rows, 70 at 8, 78 at 16, 81 at 20, 84 at 24.  (The products
 // by warp-level MMA were tried first: about 60 cycles each a warp on this part, so eight
 // warps an SM held the step at 239 us, B16 H32 8192 keys D128, floor 159.)
 //
 // Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile is
 // weighed with the references as they are; only if some score outgrew them, which one
-// barrier with a vote finds out, are new ones found and the tile weighed again.  The threads write P^T as the second product's narrow operand, one byte
-// (or 16-bit value) a row and term, and read O^T at a run's end, by when the next run's queries are in
-// place.  Warp 4: TMA producer; K and V tiles share one ring that runs on over a CTA's
+// barrier with a vote finds out, are new ones found and the tile weighed again.  The threads
+// write P^T as the second product's narrow operand, in one of two places, so that the next tile is weighed
+// while that product runs, and read O^T at a run's end, by when the next run's queries are in place.  Warp 4: TMA producer; K and V tiles share one ring that runs on over a CTA's
 // runs.  Warp 5: MMA issuer; S^T of the next tile is issued before the softmax of this one is done.
 //
 // Schedule.  The tiles of all (sequence, head, row group) units are laid out in
@@ -53,7 +55,7 @@ constexpr int kBoxKeys = 32;  // keys of one TMA box: a last tile reads no more 
 // Weights enter the terms times 2^4 and may outgrow their reference by 2^4, so that
 // they stay within 256 and the terms reach down to 2^-20 / 2^4 = 2^-24 of the reference (fp16:
 // 2^-25).  A slack of 2^1 at a scale of 2^7 found new references in every other tile
-// at 20 rows a key head (172 us against 90, 24 ragged sequences up to 16384 keys).
+// at 20 rows a key head and nearly doubled the step.
 constexpr float kWeightLog2 = 4.f;  // codes only
 constexpr float kRefSlack = 4.f;   // log2 units a weight may outgrow its reference by
 constexpr float kSumSlack = 60.f;  // the same for the float32 normaliser

@@ -270,6 +270,9 @@ SHARED = [
     (2, 9, 3, 40, 384, 260, [260, 40], 128, BF16, True, False),         # 120 rows a key head
     (300, 4, 2, 1, 130, 6, None, 128, F16, True, True),                 # 600 rows, little of their own
     (7, 2, 2, 1, 128 * 153, 20, None, 64, BF16, True, True),            # one unit over all CTAs, and then some
+    (5, 6, 6, 8, 9000, 183, None, 128, BF16, True, True),               # nearly all SMs for the prefix
+    (40, 8, 2, 5, 200, 1500, None, 64, F16, True, True),                # few for it
+    (9, 12, 2, 3, 3000, 900, None, 128, F16, True, False),
 ]
 
 
@@ -411,8 +414,7 @@ def test_scores_that_rise_along_the_cache(own8):
 
 
 def test_infinite_scores_weigh_nothing_or_everything():
-    """-inf in a 16-bit key: as if it were not there; a row of nothing else is not a number,
-    as in the definition (0 / 0)."""
+    """-inf in a 16-bit key: as if it were not there, here for a whole first tile and a part of the second."""
     D, cap = 64, 300
     q = torch.zeros(1, 1, 1, D, dtype=BF16)
     q[..., 0] = 1.0
