@@ -27,9 +27,11 @@
 // Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile is
 // weighed with the references as they are; only if some score outgrew them, which one
 // barrier with a vote finds out, are new ones found and the tile weighed again.  The threads
-// write P^T as the second product's narrow operand, in one of two places, so that the next tile is weighed
-// while that product runs, and read O^T at a run's end, by when the next run's queries are in place.  Warp 4: TMA producer; K and V tiles share one ring that runs on over a CTA's
-// runs.  Warp 5: MMA issuer; S^T of the next tile is issued before the softmax of this one is done.
+// write P^T as the second product's narrow operand, in one of two places, so that the next
+// tile is weighed while that product runs, and read O^T at a run's end, by when the next
+// run's queries are in place.  Warp 4: TMA producer; K and V tiles share one ring that runs
+// on over a CTA's runs.  Warp 5: MMA issuer; S^T of the next tile is issued before the
+// softmax of this one is done.
 //
 // Schedule.  The tiles of all (sequence, head, row group) units are laid out in
 // a row and cut into equal shares, one a CTA, from the lengths on the device; a run is
@@ -105,7 +107,8 @@ struct OwnCfg {
   static constexpr int kFit = (108 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kMost = kTileBytes <= 8192 ? 8 : 5;
-  static constexpr int kSlots = kFit >= 3 ? (kFit < kMost ? kFit : kMost) : 6;  // K of step g: 2 g, V: 2 g + 1, modulo kSlots
+  // K of step g: slot 2 g, V: 2 g + 1, modulo kSlots
+  static constexpr int kSlots = kFit >= 3 ? (kFit < kMost ? kFit : kMost) : 6;
   static constexpr int kSmem = kRingOff + kSlots * kTileBytes + kPad + 1024;
   static constexpr int kCols = 2 * kN + kPN <= 64 ? 64 : 2 * kN + kPN <= 128 ? 128 : 256;  // two S^T, O^T
   static constexpr int kChunk = R < 8 ? R : 8;                                 // rows read out together
