@@ -163,7 +163,7 @@ inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
 // How a step is laid over the SMs.  With a prefix and own rows, the two passes run
 // side by side, the prefix on as many SMs as let both end at about the same time: each pass's
 // start and end (its queries, first copies, states) hides behind the other's stream.  64 sequences behind 8192 keys,
-// 16-bit rows of up to 1024: 52 us one after the other, 45 side by side on 52 + 100 SMs (51 on 32 + 120 or 76 + 76);
+// 16-bit rows of up to 1024: 52 us one after the other, 45 side by side on 47 + 105 SMs (51 on 32 + 120 or 76 + 76);
 // 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 85, and 70 on 32 + 120 (73 on 43 + 109); 256
 // behind 32768: 132, and 121 on 128 + 24 (125 on 132 + 20).
 // The lengths are on the device, so the own rows are taken to be a little over half of
