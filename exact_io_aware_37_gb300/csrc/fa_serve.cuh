@@ -43,6 +43,22 @@ __host__ __device__ __forceinline__ int own_tiles(int len) { return (int)(((unsi
 // Cost of a unit of `tiles` tiles: the run's own cost, then a tile each.
 __device__ __forceinline__ int own_cost(const ServeArgs& a, int tiles) { return tiles > 0 ? tiles + a.run_cost : 0; }
 
+// A truth value that a generic lambda can take as a type.
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
+// Elements of a word of two 16-bit values that are not finite become zero.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite_only16(uint32_t w) {
+  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (((w >> (16 * i)) & kExp) == kExp) w &= ~(0xffffu << (16 * i));
+  return w;
+}
+
 // Factor of a state with maximum m joined under the maximum mm >= m: 1 for
 // equal maxima, -inf among them (that state holds nothing, or only NaN).
 __device__ __forceinline__ float join_factor(float m, float mm) { return m == mm ? 1.f : exp2f(m - mm); }

@@ -69,11 +69,6 @@ struct OwnParams {
   bool q_f16;  // 8-bit cache: the queries' type (16-bit caches have the queries' type)
 };
 
-template <bool B>
-struct Flag {
-  static constexpr bool value = B;
-};
-
 enum CacheKind { kE4m3, kBf16, kF16 };
 
 template <int Kind, int D, int R>
@@ -133,16 +128,10 @@ __device__ __forceinline__ float cache_value(const uint8_t* p) {
 // Elements of a word of values that are not finite become zero.
 template <int Kind>
 __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-  if constexpr (Kind == kE4m3) {
+  if constexpr (Kind != kE4m3) return finite_only16<Kind == kF16>(w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
-  } else {
-    constexpr uint32_t kExp = Kind == kBf16 ? 0x7f80u : 0x7c00u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (((w >> (16 * i)) & kExp) == kExp) w &= ~(0xffffu << (16 * i));
-  }
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
   return w;
 }
 

@@ -23,6 +23,12 @@
 // The steps of all units in a row are cut into equal runs, one a CTA, and a
 // unit's states are joined over the CTAs that share it.
 //
+// Hidden keys.  Where a sequence's own part is shorter than its new tokens, causal hides the prefix's
+// last keys from some of its rows.  Their weights are zero, but 0 * NaN is not: in the tiles
+// that some row does not see whole, the softmax warps put zeros in place of such keys' values that are not finite, and
+// the rows that do see them get them at the run's end, as in the pass over the own rows.  One slot does it for both
+// where they share the keys (its product is issued first).
+//
 // Warps and barriers are those of the forward, except that the softmax warps
 // write their own Q tile into shared memory (rows of one tile come from many
 // sequences) and announce it on bar_q[t], a run's before they read out the last one's state.
@@ -63,7 +69,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kVOff + kStages * kTileBytes + 1024;
 };
 
-template <int D, bool F16, bool kSplit>
+template <int D, bool F16, bool kSplit, bool kHide>
 __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_constant__ PrefixParams p) {
   using C = Cfg<D>;
   constexpr int kCols = kSplit ? kBN / 2 : kBN;  // keys of a slot's score tile
@@ -79,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_p[2], bar_fin[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ int s_bad;  // a hidden value was not finite, in this run or an earlier one
 
   const ServeArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -120,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
       mbar_init(&bar_fin[t], 1);
     }
     abort_flag = 0;
+    s_bad = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -143,6 +151,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t t_s = tmem + lane_off + t * 128;
     const uint32_t t_o = tmem + lane_off + 256 + t * 128;
+    // The prefix keys that row rr of a sequence with len rows of its own sees.
+    auto seen = [&](int len, int rr) -> int {
+      return a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
+    };
+    // The keys that all rows of a run's unit see (as far as the run's keys go): what the first new token of every
+    // sequence in it sees.
+    auto seen_by_all = [&](const Run& q) -> int {
+      int lim = a.np;
+      if (!kHide || (q.j0 + q.n) * kBN <= a.np - a.nq + 1) return lim;
+      const int n = min(rows - q.row0, kSplit ? kBM : 2 * kBM), b0 = q.row0 / gq, b1 = (q.row0 + n - 1) / gq;
+      for (int b = b0 + lane; b <= b1; b += 32) {
+        const int len = raw_len(a, b);
+        if (len_ok(a, len)) lim = min(lim, seen(len, 0));
+      }
+      return __reduce_min_sync(0xffffffffu, lim);
+    };
     // A run's query row to this slot's tile; kmax: the prefix keys that the row sees.
     // Every S of the slot's run before is complete.
     auto put_q = [&](const Run& q, int& kmax) {
@@ -174,8 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
                                     (((ch & 7) ^ (to & 7)) << 4)) = x[i];
         }
       }
-      if (len_ok(a, len))
-        kmax = a.causal ? (int)max(0ll, min((long long)a.np, (long long)a.np + len - a.nq + rr % a.nq + 1)) : a.np;
+      if (len_ok(a, len)) kmax = seen(len, rr);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -188,131 +211,204 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     Run q, nx;
     int kmax = 0, kmax_next = 0;
     bool have = next_run(cur, q), ready = false;
-    while (ok && have) {
-      have = next_run(cur, nx);
-      if (t < q.slots) {
-        const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;
-        if (ready)
-          kmax = kmax_next;
-        else
-          put_q(q, kmax);
-        ready = false;
-        const bool work = __any_sync(0xffffffffu, kmax > 0);  // a warp without a row only keeps step
-        float m_ref = -INFINITY;  // reference maximum of the exponentials (log2 units)
-        float l = 0.f;
-        for (int j = 0; j < q.n; ++j) {
-          const int g = G + j;
-          if (!warp_wait(&bar_s[t], cs & 1, w)) {
-            ok = false;
-            break;
-          }
-          ++cs;
-          if (t == q.slots - 1 && quad == 0 && lane == 0) {
-            // S of the last slot is complete, and with it every product issued before
-            // it: the other slot's S (K_g is consumed) and both P V of the step before
-            mbar_arrive(&bar_kfree[g % C::kStages]);
-            if (g > 0) mbar_arrive(&bar_vfree[(g - 1) % C::kStages]);
-          }
-          tc_fence_after();
-          if (work) {
-            uint32_t sr[kCols / 32][32];
+    // A run's steps and its state.  hide: some row does not see all of its keys (lim_all: those that all see).  Two
+    // copies of the loop, the second only in kernels for steps that may hide keys: 64 sequences of 20 query rows a key
+    // head behind 8192 keys of D 64 take 42.5 us (42.3 without the second; with one loop that checks every step 43.7),
+    // 64 sequences of one new token and 4 rows behind 8192 keys 47.9 (48.7 with the second loop there).
+    auto work_run = [&](auto hide, int lim_all) {
+      const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;
+      const bool work = __any_sync(0xffffffffu, kmax > 0);  // a warp without a row only keeps step
+      float m_ref = -INFINITY;  // reference maximum of the exponentials (log2 units)
+      float l = 0.f;
+      for (int j = 0; j < q.n; ++j) {
+        const int g = G + j;
+        if (!warp_wait(&bar_s[t], cs & 1, w)) {
+          ok = false;
+          break;
+        }
+        ++cs;
+        if (t == q.slots - 1 && quad == 0 && lane == 0) {
+          // S of the last slot is complete, and with it every product issued before
+          // it: the other slot's S (K_g is consumed) and both P V of the step before
+          mbar_arrive(&bar_kfree[g % C::kStages]);
+          if (g > 0) mbar_arrive(&bar_vfree[(g - 1) % C::kStages]);
+        }
+        tc_fence_after();
+        if (work) {
+          uint32_t sr[kCols / 32][32];
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
+          for (int c = 0; c < kCols / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) tmem_ld_wait(sr[c]);
-            const int k0 = (q.j0 + j) * kBN + (kSplit ? t * kCols : 0);
-            if (k0 + kCols > kmax) {
-              const int cut = kmax - k0;
-#pragma unroll
-              for (int c = 0; c < kCols / 32; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (c * 32 + e >= cut) sr[c][e] = __float_as_uint(-INFINITY);
-            }
-            float mp[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) mp[x] = -INFINITY;
+          for (int c = 0; c < kCols / 32; ++c) tmem_ld_wait(sr[c]);
+          const int k0 = (q.j0 + j) * kBN + (kSplit ? t * kCols : 0);
+          if (k0 + kCols > kmax) {
+            const int cut = kmax - k0;
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mp[(e >> 1) & 7] =
-                    fmax3(mp[(e >> 1) & 7], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
-            const float mt = fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(fmax3(mp[3], mp[4], mp[5]), mp[6], mp[7]));
-            const float m_new = fmaxf(m_ref, mt * a.c2);
-            float alpha = 1.f;
-            const bool grow = m_new > m_ref + kRescaleThreshold;
-            if (grow) {
-              alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - m_new);
-              m_ref = m_new;
-              l *= alpha;
-            }
-            const float nmu = (m_ref == -INFINITY) ? 0.f : -m_ref;
-            float rs0 = 0.f, rs1 = 0.f;
-            // P (16-bit pairs) over the scores, 32 packed columns at a time
-#pragma unroll
-            for (int hf = 0; hf < kCols / 64; ++hf) {
-              uint32_t pk[32];
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const int e0 = 64 * hf + 2 * c;
-                float a0, a1;
-                ffma2(a0, a1, __uint_as_float(sr[e0 >> 5][e0 & 31]), __uint_as_float(sr[(e0 + 1) >> 5][(e0 + 1) & 31]),
-                      a.c2, nmu, nmu);
-                const float p0 = ex2_approx(a0);
-                const float p1 = ex2_approx(a1);
-                fadd2(rs0, rs1, p0, p1);  // sums take the unrounded weights
-                pk[c] = pack16x2<F16>(p0, p1);
-              }
-              tmem_st32(t_s + 32 * hf, pk);
-            }
-            l += rs0 + rs1;
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
-              // accumulator rows rescaled in place: the previous P V is complete (the
-              // wait on bar_s covers it) and this step's waits for bar_p below
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_o + c, o);
-                tmem_ld_wait(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32(t_o + c, o);
-              }
-            }
-            tmem_st_wait();
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= cut) sr[c][e] = __float_as_uint(-INFINITY);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_p[t]);
-        }
-        // the next run's queries, while this one's last product runs: its S is issued
-        // after that product, over the weights that it has read by then
-        if (ok && have && t < nx.slots) {
-          put_q(nx, kmax_next);
-          ready = true;
-        }
-        if (ok && warp_wait(&bar_fin[t], fin & 1, w)) {
-          ++fin;
-          tc_fence_after();
-          // the run's state, in groups of eight columns: a warp's rows are neighbours there
-          const long long at = ((long long)q.part * 2 + t) * kBM;
-          if (work) {
-            float* u = a.pre_u + at * D + r * 8;
+          float mp[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) mp[x] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mp[(e >> 1) & 7] =
+                  fmax3(mp[(e >> 1) & 7], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+          const float mt = fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(fmax3(mp[3], mp[4], mp[5]), mp[6], mp[7]));
+          const float m_new = fmaxf(m_ref, mt * a.c2);
+          float alpha = 1.f;
+          const bool grow = m_new > m_ref + kRescaleThreshold;
+          if (grow) {
+            alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - m_new);
+            m_ref = m_new;
+            l *= alpha;
+          }
+          const float nmu = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          float rs0 = 0.f, rs1 = 0.f;
+          // P (16-bit pairs) over the scores, 32 packed columns at a time
+#pragma unroll
+          for (int hf = 0; hf < kCols / 64; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int e0 = 64 * hf + 2 * c;
+              float a0, a1;
+              ffma2(a0, a1, __uint_as_float(sr[e0 >> 5][e0 & 31]), __uint_as_float(sr[(e0 + 1) >> 5][(e0 + 1) & 31]),
+                    a.c2, nmu, nmu);
+              const float p0 = ex2_approx(a0);
+              const float p1 = ex2_approx(a1);
+              fadd2(rs0, rs1, p0, p1);  // sums take the unrounded weights
+              pk[c] = pack16x2<F16>(p0, p1);
+            }
+            tmem_st32(t_s + 32 * hf, pk);
+          }
+          l += rs0 + rs1;
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // accumulator rows rescaled in place: the previous P V is complete (the
+            // wait on bar_s covers it) and this step's waits for bar_p below
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld32(t_o + c, o);
               tmem_ld_wait(o);
-              if (row < rows)
 #pragma unroll
-                for (int x = 0; x < 32; x += 8) store32(u + ((c + x) >> 3) * (kBM * 8), o + x);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(t_o + c, o);
             }
           }
-          if (row < rows) a.pre_ml[at + r] = make_float4(m_ref, l, work ? m_ref : -INFINITY, 0.f);
-        } else {
-          ok = false;
+          tmem_st_wait();
         }
+        if (hide.value && (q.j0 + j + 1) * kBN > lim_all && (kSplit || t == 0)) {
+          // hidden values that are not finite; V_g stays until this slot's warps are in the next step
+          if (!warp_wait(&bar_kv[g % C::kStages], (g / C::kStages) & 1, w)) {
+            ok = false;
+            break;
+          }
+          // a key a thread; with halved keys two threads share one
+          constexpr int kChunks = D / 8 / (kSplit ? 2 : 1);
+          const int key = kSplit ? t * kCols + (r & (kCols - 1)) : r, ch0 = kSplit ? r / kCols * kChunks : 0;
+          const int at = (q.j0 + j) * kBN + key;
+          if (at >= lim_all && at < a.np) {
+            uint8_t* v = smem + C::kVOff + (g % C::kStages) * C::kTileBytes + key * 128;
+#pragma unroll 1
+            for (int c4 = ch0; c4 < ch0 + kChunks; c4 += 4) {
+              uint4 u[4];
+              auto chunk = [&](int x) {
+                return reinterpret_cast<uint4*>(v + ((c4 + x) >> 3) * C::kHalfBytes + ((((c4 + x) & 7) ^ (key & 7)) << 4));
+              };
+#pragma unroll
+              for (int x = 0; x < 4; ++x) u[x] = *chunk(x);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint4 y = make_uint4(finite_only16<F16>(u[x].x), finite_only16<F16>(u[x].y),
+                                           finite_only16<F16>(u[x].z), finite_only16<F16>(u[x].w));
+                if (u[x].x != y.x || u[x].y != y.y || u[x].z != y.z || u[x].w != y.w) {
+                  *chunk(x) = y;
+                  *reinterpret_cast<volatile int*>(&s_bad) = 1;
+                }
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_p[t]);
+      }
+      // the next run's queries, while this one's last product runs: its S is issued
+      // after that product, over the weights that it has read by then
+      if (ok && have && t < nx.slots) {
+        put_q(nx, kmax_next);
+        ready = true;
+      }
+      if (ok && warp_wait(&bar_fin[t], fin & 1, w)) {
+        ++fin;
+        tc_fence_after();
+        // the run's state, in groups of eight columns: a warp's rows are neighbours there
+        const long long at = ((long long)q.part * 2 + t) * kBM;
+        // the weights' barriers and the product's lie between the last of its writers and here
+        const bool bad = hide.value && *reinterpret_cast<volatile int*>(&s_bad) != 0;
+        if (work) {
+          float* u = a.pre_u + at * D + r * 8;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+            if (bad) {  // hidden from other rows, not from this one
+              const int k1 = min(kmax, (q.j0 + q.n) * kBN);
+#pragma unroll 1
+              for (int key = max(lim_all, q.j0 * kBN); key < k1; ++key) {
+                if (kSplit && ((key / kCols) & 1) != t) continue;  // the other slot's
+                const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.vp) +
+                                                                   ((long long)q.hk * a.np + key) * D + c);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint4 y = __ldg(from + x);
+                  const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t not_finite = yw[e] ^ finite_only16<F16>(yw[e]);  // the others: +0
+                    float2 f;
+                    if constexpr (F16)
+                      f = __half22float2(*reinterpret_cast<const __half2*>(&not_finite));
+                    else
+                      f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&not_finite));
+                    uint32_t& o0 = o[8 * x + 2 * e];
+                    uint32_t& o1 = o[8 * x + 2 * e + 1];
+                    o0 = __float_as_uint(__uint_as_float(o0) + f.x);
+                    o1 = __float_as_uint(__uint_as_float(o1) + f.y);
+                  }
+                }
+              }
+            }
+            if (row < rows)
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) store32(u + ((c + x) >> 3) * (kBM * 8), o + x);
+          }
+        }
+        if (row < rows) a.pre_ml[at + r] = make_float4(m_ref, l, work ? m_ref : -INFINITY, 0.f);
+      } else {
+        ok = false;
+      }
+    };
+    while (ok && have) {
+      have = next_run(cur, nx);
+      if (t < q.slots) {
+        if (ready)
+          kmax = kmax_next;
+        else
+          put_q(q, kmax);
+        ready = false;
+        const int lim_all = seen_by_all(q);
+        if (kHide && lim_all < a.np)
+          work_run(Flag<kHide>{}, lim_all);
+        else
+          work_run(Flag<false>{}, lim_all);
       }
       G += q.n;
       q = nx;
@@ -474,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool F16, bool kSplit>
+template <int D, bool F16, bool kSplit, bool kHide>
 cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
   using C = Cfg<D>;
   PrefixParams p;
@@ -482,16 +578,22 @@ cudaError_t launch_prefix_d(const ServeArgs& a, const PrefixPlan& plan, cudaStre
   p.plan = plan;
   if (!make_map_cache(&p.tk, a.kp, 2, D, a.np, a.Hk, kBN) || !make_map_cache(&p.tv, a.vp, 2, D, a.np, a.Hk, kBN))
     return note_error("prefix tensor map encode", cudaErrorInvalidValue);
-  const cudaError_t e = cudaFuncSetAttribute(tc_prefix_kernel<D, F16, kSplit>,
+  const cudaError_t e = cudaFuncSetAttribute(tc_prefix_kernel<D, F16, kSplit, kHide>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return note_error("prefix smem attribute", e);
-  return note_error("prefix launch", launch_serve_kernel(tc_prefix_kernel<D, F16, kSplit>, plan.ctas, kThreads,
+  return note_error("prefix launch", launch_serve_kernel(tc_prefix_kernel<D, F16, kSplit, kHide>, plan.ctas, kThreads,
                                                          C::kSmemBytes, false, s, p));
 }
 
+template <int D, bool F16, bool kHide>
+cudaError_t launch_prefix_h(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
+  return plan.split ? launch_prefix_d<D, F16, true, kHide>(a, plan, s) : launch_prefix_d<D, F16, false, kHide>(a, plan, s);
+}
+
+// One new token is the last of its sequence, and sees the whole prefix.
 template <int D, bool F16>
 cudaError_t launch_prefix_f(const ServeArgs& a, const PrefixPlan& plan, cudaStream_t s) {
-  return plan.split ? launch_prefix_d<D, F16, true>(a, plan, s) : launch_prefix_d<D, F16, false>(a, plan, s);
+  return a.causal && a.nq > 1 ? launch_prefix_h<D, F16, true>(a, plan, s) : launch_prefix_h<D, F16, false>(a, plan, s);
 }
 
 }  // namespace

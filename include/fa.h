@@ -441,7 +441,7 @@ fa_status fa_decode_cache(const void* q, const void* k_codes, const void* v_code
  *                       max_len == 0)
  * The keys of sequence b are the prefix, then its own lens[b] rows: query row i sits at position
  * np + lens[b] - nq + i of them.  Everything else is as for fa_decode_cache; the weights of 16-bit rows are rounded
- * to dtype.  Prefix values that causal hides from some of a batch's rows (where lens[b] < nq - 1) must be finite.  np + max_len <= 2^30 (FA_ERR_UNSUPPORTED). */
+ * to dtype.  np + max_len <= 2^30 (FA_ERR_UNSUPPORTED). */
 size_t fa_decode_shared_workspace_size(int B, int H, int Hk, int nq, int np, int max_len, int D, fa_dtype dtype);
 fa_status fa_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
                            const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk,

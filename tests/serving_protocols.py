@@ -201,9 +201,10 @@ def run_own(runs, seed, H=3, W=3, skip=()):
     drive(rng, {"producer": producer(), "mma": mma(), **{f"w{w}": softmax(w) for w in range(W)}}, m)
 
 
-def run_prefix(runs, seed, S=2, W=2, skip=(), one_barrier=False):
+def run_prefix(runs, seed, S=2, W=2, skip=(), one_barrier=False, scrub=False, scrub_slot=0):
     """runs: (steps, slots) of each run; S stages; W softmax warps a slot.
-    one_barrier: a run's last P V announced on the barrier of the scores."""
+    one_barrier: a run's last P V announced on the barrier of the scores.
+    scrub: the warps of scrub_slot write into V before they announce their weights, at some steps."""
     rng = random.Random(seed)
     m = Machine(rng)
     k0, kv = Bar("k0", 1), [Bar(f"kv{i}", 1) for i in range(S)]
@@ -214,6 +215,7 @@ def run_prefix(runs, seed, S=2, W=2, skip=(), one_barrier=False):
     starts = [sum(n for n, _ in runs[:i]) for i in range(len(runs))]
     read = {(t, r): 0 for t in range(2) for r in range(len(runs))}
     complete = set()  # (slot, run) whose last P V is done
+    scrubbed = [scrub and rng.random() < 0.5 for _ in range(total)]
 
     def maybe(name, gen):
         if name not in skip:
@@ -292,6 +294,10 @@ def run_prefix(runs, seed, S=2, W=2, skip=(), one_barrier=False):
                 yield
                 m.write(("SP", t, w), ("P", g))
                 yield
+                if scrubbed[g] and t == min(scrub_slot, slots - 1):
+                    yield from maybe("scrub", wait(kv[g % S], g // S))
+                    assert m.has.get(("V", g % S)) == g, "values of another step"
+                    m.write(("V", g % S), g)
                 bp[t].arrive()
             if r + 1 < len(runs) and t < runs[r + 1][1]:
                 m.write(("Q", t, w), r + 1)

@@ -56,3 +56,16 @@ def test_the_last_product_needs_a_barrier_of_its_own():
     """On the scores' barrier the next run's first S can complete a second phase
     before the softmax looks at the first: the wait then never ends."""
     assert fails(models.run_prefix, prefix_case, 200, one_barrier=True)
+
+
+@pytest.mark.parametrize("part", range(4))
+def test_prefix_protocol_holds_where_values_are_hidden(part):
+    """The first slot's warps write into V for both slots."""
+    for seed in range(100 * part, 100 * part + 100):
+        runs, S = prefix_case(seed)
+        models.run_prefix(runs, seed, S, scrub=True)
+
+
+def test_hidden_values_need_their_wait_and_the_first_slot():
+    assert fails(models.run_prefix, prefix_case, 60, scrub=True, skip=("scrub",))
+    assert fails(models.run_prefix, prefix_case, 60, scrub=True, scrub_slot=1)
