@@ -32,7 +32,7 @@ constexpr int kManyStates = 6;
 
 struct MergeParams {
   ServeArgs a;
-  int cta_rows, row_groups;  // of the pass over the own rows
+  int cta_rows, row_groups, own_ctas;  // of the pass over the own rows
   PrefixPlan pre;
 };
 
@@ -202,7 +202,7 @@ cudaError_t launch_merge(const MergeParams& p, int D, cudaStream_t s) {
   // states of a row, about: the prefix's parts, and the CTAs that share a unit of the own rows
   const long long units = (long long)p.a.B * p.a.Hk * p.row_groups;
   const long long states = (p.a.np > 0 ? (p.pre.steps / p.pre.per_cta + 1) * (p.pre.split ? 2 : 1) : 0) +
-                           std::min<long long>(kOwnCtas / units, own_tiles(p.a.max_len));
+                           std::min<long long>(p.own_ctas / units, own_tiles(p.a.max_len));
   const bool few = rows <= kFewRows && states >= kManyStates;
   const int per = kMergeThreads / (D / 8) / (few ? 4 : 1);
   auto* kernel = few ? (D == 64 ? merge_kernel<T, 64, 4> : merge_kernel<T, 128, 4>)
@@ -265,6 +265,7 @@ cudaError_t launch_serve(ServeArgs& a, int D, fa_dtype dt, void* workspace, cuda
   m.row_groups = (a.group * a.nq + m.cta_rows - 1) / m.cta_rows;
   const ServePlan plan = serve_plan(a.B, a.Hk, a.group * a.nq, a.np, a.max_len, D, a.k_exp ? 1 : 2);
   m.pre = plan.pre;
+  m.own_ctas = plan.own_sms * own_per_sm(m.cta_rows, a.k_exp ? 1 : 2, D);
   carve(a, D, m.pre, static_cast<char*>(workspace));
   cudaError_t e = cudaSuccess;
   if (a.np > 0) e = launch_prefix(a, m.pre, D, f16, s);

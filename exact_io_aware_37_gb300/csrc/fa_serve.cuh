@@ -31,6 +31,10 @@ inline int own_rows(int rows) {
   if (rows <= 16) return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   return (rows + 15) / 16 <= (rows + 23) / 24 ? 16 : 24;  // the fewest groups, then the fewest rows
 }
+// CTAs of an SM: two, but where their rings of tiles leave no room for a second (OwnCfg checks it).
+constexpr int own_per_sm(int cta_rows, int elem_bytes, int D) {
+  return cta_rows == 24 && elem_bytes == 2 && D == 128 ? 1 : 2;
+}
 
 // A length out of range counts as 0 (reported here and by the join, which leaves its rows alone).
 __device__ __forceinline__ int raw_len(const ServeArgs& a, int b) { return a.lens ? __ldg(a.lens + b) : a.max_len; }
@@ -196,17 +200,22 @@ __noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_
   s.pre = prefix_plan(B, Hk, gq, np, kSms);
   s.own_sms = kSms;
   if (!s.together) return s;
-  // Times in us, fitted to the CTAs of those and other batches.  Own rows on m SMs, two CTAs an SM: 6 to begin, a
-  // tile 1.1 (16 rows 1.2, 24 rows 1.5), a run 3 (16-bit 1, 24 rows 5), and no less than the stream at 6.5 TB/s.
-  const int rows = own_rows(gq);
+  // Times in us, fitted to the CTAs of those and other batches.  Own rows on m SMs, own_per_sm CTAs an SM: 6 to begin, a
+  // tile 1.1 (16 rows 1.2, 24 rows 1.5, or 1.2 where a CTA has its SM to itself), a run 3 (16-bit 1, 24 rows 5), and no
+  // less than the stream at 6.5 TB/s.  (Two CTAs counted where there is one: 8 sequences of 5 new tokens, 8 key heads,
+  // 65536 + up to 2048 16-bit keys took 131 us on 142 + 10 SMs, 75 on 128 + 24.)
+  const int rows = own_rows(gq), per_sm = own_per_sm(rows, elem_bytes, D);
   const double units = (double)B * Hk * ((gq + rows - 1) / rows), tiles = units * (0.55 * max_len / kOwnTile + 0.5);
-  const double tile_us = rows <= 8 ? 1.1 : rows == 16 ? 1.2 : 1.5, run_us = rows == 24 ? 5.0 : elem_bytes == 1 ? 3.0 : 1.0;
+  const double tile_us = rows <= 8 ? 1.1 : rows == 16 || per_sm == 1 ? 1.2 : 1.5;
+  const double run_us = rows == 24 ? 5.0 : elem_bytes == 1 ? 3.0 : 1.0;
   const double stream = 6 + tiles * (2.0 * kOwnTile * D * elem_bytes) / 6.5e6;
-  const double own0 = 6 + run_us, own = (tiles * tile_us + units * run_us) / 2;
+  const double own0 = 6 + run_us, own = (tiles * tile_us + units * run_us) / per_sm;
   // The prefix on n SMs: 9 at its ends, a step 1.7 with halved keys, else 1.6, or 2.2 beside a stream that takes the
-  // memory's rate.
+  // memory's rate, and 2.5 for every unit of a CTA but its first (64 sequences of 5 new tokens behind 1024 keys, 40 units
+  // of 8 steps: 59 us at 20 steps a CTA, 75 at 27, 95 at 40, 141 at 64).
+  constexpr double kUnitUs = 2.5;
   const double step_us = (s.pre.split ? 1.7 : stream - 6 > own / kSms ? 2.2 : 1.6) * (D == 128 ? 1.0 : 0.65);
-  const double steps = (double)s.pre.units * s.pre.steps, pre = steps * step_us;
+  const double steps = (double)s.pre.units * s.pre.steps, pre = steps * step_us + s.pre.units * kUnitUs;
   // own0 + own / (kSms - n) = 9 + pre / n
   const double d = own0 - 9, b = d * kSms + own + pre;
   double n = 2 * pre * kSms / (b + sqrt(b * b - 4 * d * pre * kSms));
@@ -217,7 +226,9 @@ __noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_
   for (int i = 0; i < 2; ++i) {
     const double x = floor(n) + i;
     const PrefixPlan plan = prefix_plan(B, Hk, gq, np, x < 1 ? 1 : x > kSms - 4 ? kSms - 4 : (int)x);
-    const double own_us = fmax(own0 + own / (kSms - plan.ctas), stream), us = fmax(own_us, 9 + plan.per_cta * step_us);
+    const double own_us = fmax(own0 + own / (kSms - plan.ctas), stream);
+    const double pre_us = 9 + plan.per_cta * step_us + fmax(0, (double)plan.per_cta / plan.steps - 1) * kUnitUs;
+    const double us = fmax(own_us, pre_us);
     if (i == 0 || us < best) {
       best = us;
       s.pre = plan;

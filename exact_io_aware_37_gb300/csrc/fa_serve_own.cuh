@@ -749,6 +749,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
 template <int Kind, int D, int R>
 cudaError_t launch_own_r(const ServeArgs& a, bool q_f16, int sms, bool after, cudaStream_t s) {
   using C = OwnCfg<Kind, D, R>;
+  static_assert(C::kPerSm == own_per_sm(R, C::kElem, D), "the plan counts the CTAs of an SM that the kernel has");
   OwnParams p;
   p.a = a;
   p.q_f16 = q_f16;
