@@ -307,8 +307,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
           }
 #pragma unroll
           for (int m = kRowThreads / 2; m >= 1; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
-          // scaled by a power of two to at most 224: exact in fp16 but for elements below
-          // 2^-14 / 224 of the row's largest (infinities become NaN)
+          // Scaled by a power of two to between 112 and 224 (infinities become NaN).  The terms' last step is 2^-19,
+          // so an element is off by at most 2^-20 there (and 2^-25 in fp16), 2^-26 of the row's largest: float32's own
+          // products lose as much where the largest counts, and where it meets zeros a row needs channels
+          // 2^16 apart before it shows beside a score's other roundings.
           const int eb = c8::exp_byte(big);
           const float scale = 0.5f * c8::inv_scale(eb);
           factor *= 2.f * c8::scale(eb);
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<Kind, D, R>::kPerSm) own_k
             for (int e = 0; e < C::kChunk; e += 2) {
               if constexpr (C::kCodes)
                 c8::encode2_terms(__floats2half2_rn(v[e], v[e + 1]), t[e / 2]);
-              else
+              else  // the queries' type, as the operands of one product have one type; the normaliser is not rounded
                 t[e / 2][0] = pack16x2<Kind == kF16>(v[e], v[e + 1]);
             }
             if constexpr (C::kCodes) {

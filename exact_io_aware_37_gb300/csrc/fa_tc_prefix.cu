@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
                     a.c2, nmu, nmu);
               const float p0 = ex2_approx(a0);
               const float p1 = ex2_approx(a1);
-              fadd2(rs0, rs1, p0, p1);  // sums take the unrounded weights
+              // The product takes weights of the values' type (its operands have one type), as the forward's does:
+              // half a step of it a weight.  The sums take them unrounded.
+              fadd2(rs0, rs1, p0, p1);
               pk[c] = pack16x2<F16>(p0, p1);
             }
             tmem_st32(t_s + 32 * hf, pk);

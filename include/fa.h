@@ -424,8 +424,10 @@ fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t*
  *         are never used, whatever they hold
  *   o     [B, H, nq, D] written (dtype);  lse [B, H, nq] float32, natural log
  * Query row i sits at position lens[b] - nq + i, so causal allows key j iff j <= i + lens[b] - nq.  Rows with no
- * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32; for its product with the
- * value a weight is rounded to fp16's 11 bits, down to 2^-24 of the largest contribution's.
+ * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32.  Two roundings come before
+ * the products: an element of a query is held to 2^-26 of the largest magnitude in its row (elements within 2^-16 of
+ * it exactly), and for its product with the value a weight is rounded to fp16's 11 bits, down to 2^-24 of the largest
+ * contribution's.
  * workspace: DEVICE scratch of fa_decode_cache_workspace_size(...) bytes, 256-byte aligned, owned by the caller; its
  * contents do not matter; calls (and graph replays) that overlap on the GPU need workspaces of their own. */
 size_t fa_decode_cache_workspace_size(int B, int H, int Hk, int nq, int max_len, int D, fa_dtype dtype);
@@ -440,8 +442,8 @@ fa_status fa_decode_cache(const void* q, const void* k_codes, const void* v_code
  *                       v_exp are NULL, else the 8-bit cache's codes with its exponents (may be NULL when
  *                       max_len == 0)
  * The keys of sequence b are the prefix, then its own lens[b] rows: query row i sits at position
- * np + lens[b] - nq + i of them.  Everything else is as for fa_decode_cache; the weights of 16-bit rows are rounded
- * to dtype.  np + max_len <= 2^30 (FA_ERR_UNSUPPORTED). */
+ * np + lens[b] - nq + i of them.  Everything else is as for fa_decode_cache, but that the
+ * prefix and 16-bit rows take queries as they are and weights rounded to dtype, as fa_fwd does.  np + max_len <= 2^30 (FA_ERR_UNSUPPORTED). */
 size_t fa_decode_shared_workspace_size(int B, int H, int Hk, int nq, int np, int max_len, int D, fa_dtype dtype);
 fa_status fa_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
                            const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse, int B, int H, int Hk,
