@@ -425,7 +425,7 @@ fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t*
  *   o     [B, H, nq, D] written (dtype);  lse [B, H, nq] float32, natural log
  * Query row i sits at position lens[b] - nq + i, so causal allows key j iff j <= i + lens[b] - nq.  Rows with no
  * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32.  Two roundings come before
- * the products: an element of a query is held to 2^-26 of the largest magnitude in its row (elements within 2^-16 of
+ * the products: an element of a query is held to 2^-26 of the largest magnitude in its row (elements within 2^-15 of
  * it exactly), and for its product with the value a weight is rounded to fp16's 11 bits, down to 2^-24 of the largest
  * contribution's.
  * workspace: DEVICE scratch of fa_decode_cache_workspace_size(...) bytes, 256-byte aligned, owned by the caller; its

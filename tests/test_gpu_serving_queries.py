@@ -83,4 +83,4 @@ def test_the_term_against_the_format():
             total = total + t / 32.0 ** i
             rest = (rest - t) * 32
         off = np.abs(total * 2 * 2.0 ** e - x)
-        assert np.all(off <= 2.0 ** -26 * big) and np.all(off[np.abs(x) >= 2.0 ** -16 * big] == 0)
+        assert np.all(off <= 2.0 ** -26 * big) and np.all(off[np.abs(x) >= 2.0 ** -15 * big] == 0)
