@@ -24,8 +24,10 @@ namespace {
 
 // Joins the states of every query row: D / 8 lanes a row, eight columns each, one
 // whole sector of a state's row.  The join waits for L2 more than it moves bytes, so
-// where few rows have many states kGroups groups of lanes share a row's (2048 rows of 7 states:
-// four groups 45 us a step, one 50; 3840 rows of 2: 87 and 81; 8192 rows of 5: 132 and 121).
+// where few rows have many states kGroups groups of lanes share a row's.  Four groups and one, us a step: behind a prefix
+// of 16384 keys 512 rows 32 and 62, 2048 rows 32 and 46, 4096 rows 45 and 47, 8192 rows 72 and 65; 4096 rows behind 1024
+// keys 19 and 20, 8192 rows 26 and 18.  Of the own rows alone, 16384 keys: 32 rows (about 38 states each) 15 and 20, 128 rows (9)
+// 31 and 32, 256 rows (4) and 512 rows (2) alike.
 constexpr int kMergeThreads = 256;
 constexpr long long kFewRows = 4096;
 constexpr int kManyStates = 6;

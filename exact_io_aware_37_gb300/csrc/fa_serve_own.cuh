@@ -97,8 +97,8 @@ struct OwnCfg {
   static constexpr int kPad = D == 64 ? kTileBytes : 0;
   // as many slots as leave room for a second CTA on the SM (228 KB; each also takes 1 KB of the
   // system's, 1 KB for alignment and up to 3 KB below), if that is three (a third CTA, at the same
-  // bytes in flight, gained nothing).  No more than 80 KB: with six slots of 16 KB B16 H32 8192 keys took 159 us
-  // where five take 156 and four 159.5.
+  // bytes in flight, gained nothing).  No more than 80 KB: of four, five and six slots of 16 KB five are the fastest or
+  // within 0.3 us of it over 15 shapes (B16 H32 8192 keys 160.5, 158, 160; B24 of 16384 keys, 8 key heads, 8 rows 80.7, 79.6, 82.0).
   static constexpr int kFit = (108 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kMost = kTileBytes <= 8192 ? 8 : 5;

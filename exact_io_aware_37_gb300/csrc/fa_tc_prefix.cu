@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
     Run q, nx;
     int kmax = 0, kmax_next = 0;
     bool have = next_run(cur, q), ready = false;
-    // A run's steps and its state.  hide: some row does not see all of its keys (lim_all: those that all see).  Two
-    // copies of the loop, the second only in kernels for steps that may hide keys: 64 sequences of 20 query rows a key
-    // head behind 8192 keys of D 64 take 42.5 us (42.3 without the second; with one loop that checks every step 43.7),
-    // 64 sequences of one new token and 4 rows behind 8192 keys 47.9 (48.7 with the second loop there).
+    // A run's steps and its state.  hide: some row may not see all of its keys (lim_all: those that all see).  Steps that
+    // cannot hide any have kernels without it.  Where a slot holds pairs of tiles the loop is there twice, chosen by
+    // run: 64 sequences of 20 query rows a key head behind 8192 keys of D 64 take 42.4 us (42.3 without hide; one loop
+    // 43.7).  With halved keys one loop is better: 32 of 4 rows behind 4096 keys 73.0 us (72.9 without; two loops 74.6).
     auto work_run = [&](auto hide, int lim_all) {
       const int row = q.row0 + (kSplit ? 0 : t * kBM) + r;
       const bool work = __any_sync(0xffffffffu, kmax > 0);  // a warp without a row only keeps step
@@ -407,10 +407,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_prefix_kernel(const __grid_con
           put_q(q, kmax);
         ready = false;
         const int lim_all = seen_by_all(q);
-        if (kHide && lim_all < a.np)
+        if constexpr (kHide && !kSplit) {
+          if (lim_all < a.np)
+            work_run(Flag<true>{}, lim_all);
+          else
+            work_run(Flag<false>{}, lim_all);
+        } else {
           work_run(Flag<kHide>{}, lim_all);
-        else
-          work_run(Flag<false>{}, lim_all);
+        }
       }
       G += q.n;
       q = nx;
