@@ -428,6 +428,9 @@ fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t*
  * the products: an element of a query is held to 2^-26 of the largest magnitude in its row (elements within 2^-15 of
  * it exactly), and for its product with the value a weight is rounded to fp16's 11 bits, down to 2^-24 of the largest
  * contribution's.
+ * Scores (scale * q k) have to stay below 2^23 in magnitude: there float32 still counts the log2 units that weights are
+ * found from in whole numbers; beyond, outputs are unspecified.  (Infinite scores are not: -inf is a key of no weight,
+ * +inf makes its row NaN.)
  * workspace: DEVICE scratch of fa_decode_cache_workspace_size(...) bytes, 256-byte aligned, owned by the caller; its
  * contents do not matter; calls (and graph replays) that overlap on the GPU need workspaces of their own. */
 size_t fa_decode_cache_workspace_size(int B, int H, int Hk, int nq, int max_len, int D, fa_dtype dtype);

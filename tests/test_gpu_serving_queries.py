@@ -84,3 +84,42 @@ def test_the_term_against_the_format():
             rest = (rest - t) * 32
         off = np.abs(total * 2 * 2.0 ** e - x)
         assert np.all(off <= 2.0 ** -26 * big) and np.all(off[np.abs(x) >= 2.0 ** -15 * big] == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", ["own8", "own16", "prefix"])
+@pytest.mark.parametrize("dtype, D", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("size", [1e5, 8e6, -8e6])
+def test_scores_up_to_the_stated_size(where, dtype, D, size):
+    """Exact scores of up to 2^23 in magnitude: the largest decides, and ties share.
+    Queries and keys are small whole numbers and the scale a power of two, so that a score is a multiple of the scale,
+    the same whatever its sum's order.  The scale is at least 64, and float32 is off by less than two log2 units at this
+    size, so a smaller score's weight is below e^-62 and only the largest (one, or two tied ones of the same bits) count."""
+    n = 300
+    g = torch.Generator().manual_seed(7)
+    q = torch.randint(-1, 2, (1, 2, 1, D), generator=g).float()
+    k = torch.randint(-4, 5, (1, 1, n, D), generator=g).float()
+    k[0, 0, 200] = k[0, 0, 13]                              # for D = 128 the largest of the first row, in another tile
+    v = torch.randn(1, 1, n, D, generator=g).to(torch.float8_e4m3fn).float()
+    if size < 0:                                            # all scores far below zero
+        q[..., 0], k[..., 0] = 16.0, -64.0
+    dots = q.view(2, D).double() @ k.view(n, D).double().T
+    scale = 2.0 ** np.floor(np.log2(abs(size) / float(dots.abs().max())))
+    assert float(dots.abs().max()) * scale < 2.0 ** 23 and scale >= 64 and (size > 0 or float(dots.max()) < -500)
+    qd, kd, vd = (x.to(dtype).to(DEV) for x in (q, k, v))
+    none = torch.empty(1, 0, D, dtype=dtype, device=DEV)
+    if where == "own8":
+        o, lse = fa.decode_cache(qd, cache_of(k, v), scale=scale)
+    elif where == "own16":
+        o, lse = fa.decode_shared(qd, none, none, (kd, vd), scale=scale)
+    else:
+        o, lse = fa.decode_shared(qd, kd[0], vd[0], (none[None], none[None]), scale=scale)
+    assert ok()
+    w = (dots == dots.amax(-1, keepdim=True)).double()
+    w /= w.sum(-1, keepdim=True)
+    O, A = (w @ v.view(n, D).double()).numpy(), (w @ v.view(n, D).double().abs()).numpy()
+    u = torch.finfo(dtype).eps / 2                          # of a weight and of the output; 2^-20 for the rest
+    assert (np.abs(f64(o).reshape(2, D) - O) <= (u + 2.0 ** -20) * A + u * np.abs(O)).all()
+    # the scale's factor to log2 units, the maximum and its way back: half a step of 2^-23 each
+    L = torch.logsumexp(dots * scale, -1).numpy()
+    assert (np.abs(f64(lse).reshape(2) - L) <= 2.0 ** -21 * (1 + np.abs(L))).all()
