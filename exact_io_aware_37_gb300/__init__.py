@@ -500,7 +500,7 @@ def fa_decode_cache(q, cache, lens, o, lse, causal, scale=None, max_len=None, wo
     None: max_len) of each sequence, the new tokens' rows among them.  H must be
     a multiple of the cache's Hk; query head h reads key head h // (H // Hk).
     Query i is at position lens[b] - nq + i.  max_len (default: the capacity)
-    bounds lens.  Writes o (dtype of q) and lse [B, H, nq] (float32); rows that
+    bounds lens; the scratch and the work are laid out by it.  Writes o (dtype of q) and lse [B, H, nq] (float32); rows that
     see no key get 0 and -inf."""
     if len(cache) != 4:
         raise ValueError("the cache must be a Cache8")
@@ -527,7 +527,8 @@ def fa_decode_shared(q, k_prefix, v_prefix, cache, lens, o, lse, causal, scale=N
     keys: k_prefix, v_prefix [Hk, np, D] (dtype of q), then lens[b] rows of
     each sequence's own, in `cache`: a Cache8, or a pair k, v [B, Hk, cap, D] of
     q's dtype.  Query i is at position np + lens[b] - nq + i.  Everything else
-    as for fa_decode_cache."""
+    as for fa_decode_cache.  Give max_len where the cache is much longer than its
+    sequences are: the SMs are shared out between prefix and own rows by it."""
     _serve_call("fa_decode_shared", q, (k_prefix, v_prefix), cache, lens, o, lse, causal, scale, max_len,
                 workspace, stream)
 

@@ -1,8 +1,8 @@
 // Writing and reading the 8-bit key/value cache (format: fa_cache8.cuh).
 //
 // Both kernels move rows once and compute next to nothing, so HBM traffic
-// bounds them: 4096 new rows of B2 H32 D128 bf16 are written in 30.1 us (6.7 TB/s), 8192 rows of B4 read
-// back in 117 us (6.9 TB/s).  D / 16 neighbouring threads share a row, sixteen elements each in
+// bounds them: 4096 new rows of B2 H32 D128 bf16 are written in 30.4 us (6.6 TB/s), 8192 rows of B4 read
+// back in 118 us (6.9 TB/s).  D / 16 neighbouring threads share a row, sixteen elements each in
 // pieces of 16 bytes of the dense tensor, piece p of lane x at (p D / 16 + x) pieces, so that every access of
 // a warp covers whole rows; a write finds the row's largest magnitude with xor shuffles.
 // A thread has kRows rows in flight at once, its loads ahead of the look-up of where they go.
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const Params p) {
 #pragma unroll
     for (int m = R::kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, m));
     // Infinities count as nothing too, and the conversion, which would saturate them, is to see NaN: mended where a
-    // row holds one.  (A test of every element made the ALU the bound: 35.7 us, and 30.1 without, for 4096 new rows of B2
+    // row holds one.  (A test of every element made the ALU the bound: 35.7 us, and 30.4 without, for 4096 new rows of B2
     // H32 D128 bf16.)
     if (amax == INFINITY) {
       amax = 0.f;

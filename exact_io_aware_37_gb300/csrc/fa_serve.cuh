@@ -183,11 +183,13 @@ inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
 // How a step is laid over the SMs.  With a prefix and own rows, the two passes run
 // side by side, the prefix on as many SMs as let both end at about the same time: each pass's
 // start and end (its queries, first copies, states) hides behind the other's stream.  64 sequences behind 8192 keys,
-// 16-bit rows of up to 1024: 52 us one after the other, 45 side by side on 47 + 105 SMs (51 on 32 + 120 or 76 + 76);
-// 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 85, and 70 on 32 + 120 (73 on 43 + 109); 256
-// behind 32768: 132, and 121 on 128 + 24 (125 on 132 + 20).
-// The lengths are on the device, so the own rows are taken to be a little over half of
-// max_len: shorter ones end early and leave the rest to the prefix's few SMs.
+// 16-bit rows of up to 1024: 60 us one after the other, 46 side by side on 52 + 100 SMs (50 on 43 + 109 or 76 + 76);
+// 4 drafted tokens of 32 behind 4096, 8-bit rows of up to 2048: 94, and 73 on 32 + 120 (98 on 24 + 128, 79 on 57 + 95); 256
+// behind 32768: 134, and 120 on 128 + 24 (132 on 124 + 28, 126 on 132 + 20).
+// The lengths are on the device, so the own rows are taken to be a little over half of max_len, the mean of
+// lengths spread evenly below it.  That is a guess, and max_len the caller's means to better it: shorter rows end
+// early and leave the rest to the prefix's few SMs.  Up to 200 16-bit rows of 64 sequences behind 8192 keys: 35 us with max_len
+// 200 or 1024, 80 with 4096, 132 with 8192, 420 with 32768 (8-bit rows: 29, 40, 51, 79, 214).
 // The workspace's size and the launch have to get the same plan: one copy of the arithmetic, never inlined.
 struct ServePlan {
   PrefixPlan pre;

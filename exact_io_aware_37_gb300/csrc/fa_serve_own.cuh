@@ -18,11 +18,11 @@
 // normaliser sums the unrounded 2^(s - ref_l).
 //
 // Bound.  Every cache row is read once: HBM.  Per 128 keys of D = 128 codes the
-// tensor core spends 256 cycles, the copies at the full rate 1400: B16 H32 8192 keys D128 take 158 us a step (6.8
-// TB/s).  From some 8 query rows a key head on the softmax warps' instructions show: 24 sequences of up to 16384
-// keys, 8 key heads, floor 60 us, take 62 at 4 rows, 70 at 8, 78 at 16, 81 at 20, 84 at 24.  (The products
+// tensor core spends 256 cycles, the copies at the full rate 1400: B16 H32 8192 keys D128 take 160 us a step (6.7
+// TB/s).  24 sequences of up to 16384 keys, 8 key heads, 60 us at the copy rate, take 71 at 4 query rows a key head,
+// 72 at 8, 76 at 16, 84 at 20, 85 at 24: there the softmax warps issue 38 % of the SM's slots and wait for the rest.  (The products
 // by warp-level MMA were tried first: about 60 cycles each a warp on this part, so eight
-// warps an SM held the step at 239 us, B16 H32 8192 keys D128, floor 159.)
+// warps an SM held the step at 239 us, B16 H32 8192 keys D128.)
 //
 // Roles (6 warps).  Warps 0-3: softmax, one key (its S^T lane) a thread.  A tile is
 // weighed with the references as they are; only if some score outgrew them, which one
@@ -98,7 +98,7 @@ struct OwnCfg {
   // as many slots as leave room for a second CTA on the SM (228 KB; each also takes 1 KB of the
   // system's, 1 KB for alignment and up to 3 KB below), if that is three (a third CTA, at the same
   // bytes in flight, gained nothing).  No more than 80 KB: of four, five and six slots of 16 KB five are the fastest or
-  // within 0.3 us of it over 15 shapes (B16 H32 8192 keys 160.5, 158, 160; B24 of 16384 keys, 8 key heads, 8 rows 80.7, 79.6, 82.0).
+  // within 0.3 us of it over 15 shapes (B16 H32 8192 keys: four 1.5 % slower, six 1.3 %; B24 of up to 16384 keys, 8 key heads, 8 rows: 1.5 and 3 %).
   static constexpr int kFit = (108 * 1024 - kRingOff - kPad) / kTileBytes;
   static constexpr int kPerSm = kFit >= 3 ? 2 : 1;
   static constexpr int kMost = kTileBytes <= 8192 ? 8 : 5;

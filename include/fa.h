@@ -422,6 +422,8 @@ fa_status fa_cache_read(const void* k_codes, const void* v_codes, const uint8_t*
  *         reads key head h / (H / Hk); H must be a multiple of Hk (FA_ERR_INVALID)
  *   lens  keys of each sequence, 0 <= lens[b] <= max_len <= cap; NULL: max_len each.  Rows at and after lens[b]
  *         are never used, whatever they hold
+ *   max_len  bounds lens for this call.  Behind a shared prefix the SMs are shared out by it (the lengths are on the
+ *         device): a bound near the longest length is worth more there than the cache's capacity
  *   o     [B, H, nq, D] written (dtype);  lse [B, H, nq] float32, natural log
  * Query row i sits at position lens[b] - nq + i, so causal allows key j iff j <= i + lens[b] - nq.  Rows with no
  * allowed key get O = 0 and lse = -inf.  Scores, softmax statistics and sums are float32.  Two roundings come before
