@@ -166,18 +166,25 @@ struct PrefixPlan {
   int ctas, parts;        // parts: states kept for a unit (CTAs that may share it)
   long long per_cta;
 };
+// `per` steps a CTA, or as few as that many CTAs need.
+inline PrefixPlan prefix_plan_of(PrefixPlan p, long long per) {
+  const long long all = (long long)p.units * p.steps;
+  p.ctas = (int)((all + per - 1) / per);
+  p.per_cta = (all + p.ctas - 1) / p.ctas;
+  p.ctas = (int)((all + p.per_cta - 1) / p.per_cta);
+  p.parts = (int)((p.steps - 1) / p.per_cta) + 2;
+  return p;
+}
+// On `ctas` CTAs at most.
 inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
-  PrefixPlan p;
+  PrefixPlan p = {};
   const long long rows = (long long)B * gq;
   p.split = rows <= kPrefixRows;
   p.pairs = (int)((rows + 2 * kPrefixRows - 1) / (2 * kPrefixRows));
   p.steps = (np + kPrefixKeys - 1) / kPrefixKeys;
   p.units = p.pairs * Hk;
   const long long all = (long long)p.units * p.steps;
-  p.per_cta = (all + ctas - 1) / ctas;
-  p.ctas = p.per_cta > 0 ? (int)((all + p.per_cta - 1) / p.per_cta) : 0;
-  p.parts = p.per_cta > 0 ? (int)((p.steps - 1) / p.per_cta) + 2 : 0;
-  return p;
+  return all > 0 ? prefix_plan_of(p, (all + ctas - 1) / ctas) : p;
 }
 
 // How a step is laid over the SMs.  With a prefix and own rows, the two passes run
@@ -188,8 +195,8 @@ inline PrefixPlan prefix_plan(int B, int Hk, int gq, int np, int ctas) {
 // behind 32768: 134, and 120 on 128 + 24 (132 on 124 + 28, 126 on 132 + 20).
 // The lengths are on the device, so the own rows are taken to be a little over half of max_len, the mean of
 // lengths spread evenly below it.  That is a guess, and max_len the caller's means to better it: shorter rows end
-// early and leave the rest to the prefix's few SMs.  Up to 200 16-bit rows of 64 sequences behind 8192 keys: 35 us with max_len
-// 200 or 1024, 80 with 4096, 132 with 8192, 420 with 32768 (8-bit rows: 29, 40, 51, 79, 214).
+// early and leave the rest to the prefix's few SMs.  Up to 200 16-bit rows of 64 sequences behind 8192 keys: 30 us with max_len
+// 200, 36 with 1024, 80 with 4096, 132 with 8192, 420 with 32768 (8-bit rows: 29, 40, 51, 63, 214).
 // The workspace's size and the launch have to get the same plan: one copy of the arithmetic, never inlined.
 struct ServePlan {
   PrefixPlan pre;
@@ -203,38 +210,63 @@ __noinline__ inline ServePlan serve_plan(int B, int Hk, int gq, int np, int max_
   s.own_sms = kSms;
   if (!s.together) return s;
   // Times in us, fitted to the CTAs of those and other batches.  Own rows on m SMs, own_per_sm CTAs an SM: 6 to begin, a
-  // tile 1.1 (16 rows 1.2, 24 rows 1.5, or 1.2 where a CTA has its SM to itself), a run 3 (16-bit 1, 24 rows 5), and no
-  // less than the stream at 6.5 TB/s.  (Two CTAs counted where there is one: 8 sequences of 5 new tokens, 8 key heads,
-  // 65536 + up to 2048 16-bit keys took 131 us on 142 + 10 SMs, 75 on 128 + 24.)
+  // tile 1.1 (16 rows 1.2, 24 rows 1.5), a run 3 (16-bit 1, 24 rows 5), and no less than the stream at 6.5 TB/s.  Tiles of 64 KB
+  // (D = 128 in 16 bits) 1.7 (4096 of them on 15, 30, 50 SMs: 241, 128, 84 us at 4 rows, 256, 135, 89 at 16); where a CTA has its
+  // SM to itself 1.2 alone (343, 180, 114 at 20 rows), 1.5 beside a prefix, a run 3.  (Two CTAs counted where there is one: 8
+  // sequences of 5 new tokens, 8 key heads, 65536 + up to 2048 16-bit keys took 131 us on 142 + 10 SMs, 75 on 128 + 24.)
   const int rows = own_rows(gq), per_sm = own_per_sm(rows, elem_bytes, D);
   const double units = (double)B * Hk * ((gq + rows - 1) / rows), tiles = units * (0.55 * max_len / kOwnTile + 0.5);
-  const double tile_us = rows <= 8 ? 1.1 : rows == 16 || per_sm == 1 ? 1.2 : 1.5;
-  const double run_us = rows == 24 ? 5.0 : elem_bytes == 1 ? 3.0 : 1.0;
+  const double tile_us = D * elem_bytes == 256 ? (per_sm == 1 ? 1.5 : 1.7) : rows <= 8 ? 1.1 : rows == 16 ? 1.2 : 1.5;
+  const double run_us = per_sm == 1 ? 3.0 : rows == 24 ? 5.0 : elem_bytes == 1 ? 3.0 : 1.0;
   const double stream = 6 + tiles * (2.0 * kOwnTile * D * elem_bytes) / 6.5e6;
   const double own0 = 6 + run_us, own = (tiles * tile_us + units * run_us) / per_sm;
   // The prefix on n SMs: 9 at its ends, a step 1.7 with halved keys, else 1.6, or 2.2 beside a stream that takes the
-  // memory's rate, and 2.5 for every unit of a CTA but its first (64 sequences of 5 new tokens behind 1024 keys, 40 units
-  // of 8 steps: 59 us at 20 steps a CTA, 75 at 27, 95 at 40, 141 at 64).
-  constexpr double kUnitUs = 2.5;
+  // memory's rate, and 2.5 for every further unit that a CTA touches (64 sequences of 5 new tokens behind 1024 keys, 40
+  // units of 8 steps: 59 us at 20 steps a CTA, 75 at 27, 95 at 40, 141 at 64).
+  // And the join 0.25 a state (4 sequences of 24 query rows a key head behind 5000 keys: 23 us with 20 states a row, 26 with 40, 36 with 80).
+  constexpr double kUnitUs = 2.5, kStateUs = 0.25;
   const double step_us = (s.pre.split ? 1.7 : stream - 6 > own / kSms ? 2.2 : 1.6) * (D == 128 ? 1.0 : 0.65);
   const double steps = (double)s.pre.units * s.pre.steps, pre = steps * step_us + s.pre.units * kUnitUs;
   // own0 + own / (kSms - n) = 9 + pre / n
   const double d = own0 - 9, b = d * kSms + own + pre;
   double n = 2 * pre * kSms / (b + sqrt(b * b - 4 * d * pre * kSms));
   if (own0 + own / (kSms - n) < stream && stream > 9 + pre / n) n = pre / (stream - 9);
-  // The CTAs take whole steps: of the two whole n beside it the one whose longer pass is the shorter (5 sequences of 8 new
-  // tokens, 30 key heads, 28414 + up to 183 keys: 100 us on 148 + 4 SMs, 89 on 145 + 7).
-  double best = 0;
-  for (int i = 0; i < 2; ++i) {
-    const double x = floor(n) + i;
-    const PrefixPlan plan = prefix_plan(B, Hk, gq, np, x < 1 ? 1 : x > kSms - 4 ? kSms - 4 : (int)x);
-    const double own_us = fmax(own0 + own / (kSms - plan.ctas), stream);
-    const double pre_us = 9 + plan.per_cta * step_us + fmax(0, (double)plan.per_cta / plan.steps - 1) * kUnitUs;
-    const double us = fmax(own_us, pre_us);
-    if (i == 0 || us < best) {
+  // The CTAs take whole steps: of the two whole n beside it and the cuts nearest to them that fall on the units' ends
+  // or divide the units evenly, the one whose longer pass is the shortest (5 sequences of 8 new tokens, 30 key heads, 28414 + up
+  // to 183 keys: 100 us on 148 + 4 SMs, 89 on 145 + 7; 2 sequences of 8 new tokens and 7 key heads, units of 10 steps: 22.4 us
+  // with 3 steps a CTA, 18.5 with 2; 61 of 5, units of 7: 26.5 with 6, 23.9 with 7).
+  double best = -1;
+  auto weigh = [&](long long per) {
+    const PrefixPlan plan = prefix_plan_of(s.pre, per);
+    if (plan.ctas > kSms - 4) return;
+    const long long n_steps = plan.steps, p = plan.per_cta;
+    const long long further = n_steps % p == 0 ? 0 : p % n_steps == 0 ? p / n_steps - 1 : (p + n_steps - 2) / n_steps;
+    const double join = kStateUs * (n_steps / p) * (plan.split ? 2 : 1);
+    const double us = fmax(fmax(own0 + own / (kSms - plan.ctas), stream), 9 + p * step_us + further * kUnitUs) + join;
+    if (best < 0 || us < best) {
       best = us;
       s.pre = plan;
     }
+  };
+  const long long all = (long long)s.pre.units * s.pre.steps, n_steps = s.pre.steps;
+  const long long few = n < 1 ? 1 : n > kSms - 5 ? kSms - 5 : (long long)n;
+  const long long high = (all + few - 1) / few, low = (all + few) / (few + 1);  // steps a CTA
+  weigh(high);
+  weigh(low);
+  if (low >= n_steps) {
+    weigh(low / n_steps * n_steps);
+    weigh((high + n_steps - 1) / n_steps * n_steps);
+  } else {
+    for (long long k = 1; k <= 16 && low - k > 0; ++k)
+      if (n_steps % (low - k) == 0) {
+        weigh(low - k);
+        break;
+      }
+    for (long long k = 1; k <= 16 && high + k <= n_steps; ++k)
+      if (n_steps % (high + k) == 0) {
+        weigh(high + k);
+        break;
+      }
   }
   s.own_sms = kSms - s.pre.ctas;
   return s;
